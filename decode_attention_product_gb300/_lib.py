@@ -18,12 +18,18 @@ AQ_OK = 0
 STATUS_NAMES = {0: "AQ_OK", 1: "AQ_ERR_INVALID_ARGUMENT", 2: "AQ_ERR_UNSUPPORTED",
                 3: "AQ_ERR_WORKSPACE_TOO_SMALL", 4: "AQ_ERR_CUDA"}
 DEV_BAD_PAGE, DEV_BAD_LENGTH, DEV_BAD_SET, DEV_TIMEOUT, DEV_INVARIANT = 1, 2, 4, 8, 16
+DEV_NO_PAGE, DEV_BAD_ROW = 32, 64
 STEP_OVERLAP = 1
 STEP_E4M3 = 2
+ROPE_INTERLEAVED, ROPE_TRANSPOSE, ROPE_LENGTHS = 1, 2, 4
+ROPE_SCALINGS = {"plain": 0, "linear": 1, "ntk": 2, "yarn": 3}
+Q8_INT8, Q8_E4M3 = 0, 1
+MAX_POOLS = 256
 
 # every symbol include/aqpq.h declares, with its ctypes signature
 P = ctypes.c_void_p
 i32, i64, sz, f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
+f64 = ctypes.c_double
 SIGNATURES = {
     "aq_status_string": ([i32], ctypes.c_char_p),
     "aq_last_error_message": ([], ctypes.c_char_p),
@@ -50,12 +56,27 @@ SIGNATURES = {
     "aq_decode_step_mixed_workspace": ([P, i32, i32, i32, i32, i32, P], i32),
     "aq_decode_attention_noalloc": ([P, i32, i32, i32, P, P, i64, P, i64, P, P, i32, P, i32, f32,
                                      i32, P, P, P], i32),
+    "aq_rope": ([P, i32, i32, i32, P, P, i32, f32, i32, P, P, P, P, P], i32),
+    "aq_rope_frequencies": ([i32, f64, i32, f64, i32, f64, f64, P, P], i32),
+    "aq_q8_append": ([P, i32, i32, i32, i32, P, P, P, i64, P, i32, P, P, P, P], i32),
+    "aq_q8_load": ([P, i32, i32, i32, i32, P, P, P, i64, P, i32, P, P, P, P], i32),
+    "aq_q8_decode_plan": ([P, i32, i32, i32, i32, i32, P, P], i32),
+    "aq_q8_decode_attention": ([P, i32, i32, i32, i32, P, P, P, i64, P, i32, P, i32, f32, i32, P, P, sz, P, P], i32),
+    "aq_pages_workspace": ([i32, i64, P], i32),
+    "aq_pages_extend": ([i32, P, P, P, i32, i32, P, P, i64, P, i32, P, sz, P, P], i32),
+    "aq_pages_fork": ([i32, P, P, P, i32, i32, P, P, i64, P, sz, P, P], i32),
+    "aq_pages_free": ([i32, P, P, P, i32, i32, P, P, i64, P, P], i32),
+    "aq_pages_compact": ([P, i32, i32, P, P, i64, P, i32, P, sz, P, P], i32),
 }
 
 
 class PQConfig(ctypes.Structure):
     _fields_ = [("head_dim", ctypes.c_int32), ("num_subspaces", ctypes.c_int32),
                 ("num_codewords", ctypes.c_int32), ("page_size", ctypes.c_int32)]
+
+
+class PagePool(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("page_bytes", ctypes.c_int64)]
 
 
 class AQError(RuntimeError):

@@ -7,6 +7,7 @@ arithmetic of the method happens here.  Names follow include/aqpq.h.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -333,6 +334,414 @@ def decode_attention_fp16(q: torch.Tensor, kv_pages: torch.Tensor, block_table: 
     return out
 
 
+# --------------------------------------------------------------------------
+# rotary positions
+# --------------------------------------------------------------------------
+def _launch(dev: int, name: str, *args) -> None:
+    """Call the library's `name` with args and the stream, `dev` current."""
+    fn = getattr(_lib.load(), name)
+    stream = torch._C._cuda_getCurrentRawStream(dev)
+    if torch._C._cuda_getDevice() == dev:
+        st = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, stream)
+    if st != _lib.AQ_OK:
+        _lib.check(st, name)
+
+
+def _addr(t):
+    return t.data_ptr() if t is not None else None
+
+
+@functools.lru_cache(maxsize=None)
+def _cfg_ref(head_dim: int = HEAD_DIM, page_size: int = PAGE):
+    return ctypes.byref(_lib.config(4, head_dim=head_dim, page_size=page_size))
+
+
+def _shape(t, want, name):
+    if t.shape != want:
+        raise ValueError(f"{name} must have shape {tuple(want)}, got {tuple(t.shape)}")
+
+
+def rope_frequencies(rot_dim: int = HEAD_DIM, base: float = 10000.0, scaling: str = "plain", factor: float = 1.0,
+                     original_len: int = 0, beta_fast: float = 32.0, beta_slow: float = 1.0, device="cuda"):
+    """(inv_freq float64 [rot_dim / 2] on `device`, mscale) for rope(); scaling
+    is "plain", "linear", "ntk" or "yarn" (see aq_rope_frequencies)."""
+    if scaling not in _lib.ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(_lib.ROPE_SCALINGS)}, got {scaling!r}")
+    w = (ctypes.c_double * (HEAD_DIM // 2))()
+    m = ctypes.c_float()
+    st = _lib.load().aq_rope_frequencies(rot_dim, base, _lib.ROPE_SCALINGS[scaling], factor, original_len, beta_fast,
+                                         beta_slow, w, ctypes.byref(m))
+    _lib.check(st, "aq_rope_frequencies")
+    return torch.tensor(list(w)[:rot_dim // 2], dtype=torch.float64, device=device), m.value
+
+
+def _out_of_place(t, out, name):
+    """`out` is `t` itself or memory of its own."""
+    a, b = t.data_ptr(), out.data_ptr()
+    n = t.numel() * t.element_size()
+    if a != b and a < b + n and b < a + n:
+        raise ValueError(f"{name} overlaps its input without being it")
+
+
+def rope(positions: torch.Tensor, inv_freq: torch.Tensor, q: torch.Tensor | None = None,
+         kv: torch.Tensor | None = None, interleaved: bool = False, mscale: float = 1.0, transpose: bool = False,
+         lengths: bool = False, q_out: torch.Tensor | None = None, kv_out: torch.Tensor | None = None):
+    """Rotary positions of q [T][Hq][D] fp32 and of the keys of kv [T][Hkv][2][D]
+    fp16 (either may be None): returns (q_out, kv_out), new tensors unless
+    given (q_out=q, kv_out=kv work in place).  positions int32 [T], negative for
+    padding; with lengths=True they are sequence lengths and token t stands at
+    positions[t] - 1.  transpose=True is the gradient of the plain rotation."""
+    _need(positions, torch.int32, "positions", 1)
+    _need(inv_freq, torch.float64, "inv_freq", 1)
+    T, D = positions.shape[0], HEAD_DIM
+    if q is None and kv is None:
+        raise ValueError("q or kv is required")
+    Hq = Hkv = 0
+    if q is not None:
+        _need(q, torch.float32, "q", 3)
+        Hq, D = q.shape[1], q.shape[2]
+        _shape(q, (T, Hq, D), "q")
+        if q_out is None:
+            q_out = torch.empty_like(q)
+        elif q_out is not q:
+            _need(q_out, torch.float32, "q_out", 3)
+            _shape(q_out, q.shape, "q_out")
+            _out_of_place(q, q_out, "q_out")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if kv is not None:
+        _need(kv, torch.float16, "kv", 4)
+        Hkv = kv.shape[1]
+        D = kv.shape[3] if q is None else D
+        _shape(kv, (T, Hkv, 2, D), "kv")
+        if kv_out is None:
+            kv_out = torch.empty_like(kv)
+        elif kv_out is not kv:
+            _need(kv_out, torch.float16, "kv_out", 4)
+            _shape(kv_out, kv.shape, "kv_out")
+            _out_of_place(kv, kv_out, "kv_out")
+    elif kv_out is not None:
+        raise ValueError("kv_out without kv")
+    dev = _same_device(positions, inv_freq=inv_freq, q=q, kv=kv, q_out=q_out, kv_out=kv_out)
+    _launch(dev, "aq_rope", _cfg_ref(D), T, Hq, Hkv, positions.data_ptr(), inv_freq.data_ptr(),
+            2 * inv_freq.shape[0], mscale,
+            (_lib.ROPE_INTERLEAVED if interleaved else 0) | (_lib.ROPE_TRANSPOSE if transpose else 0)
+            | (_lib.ROPE_LENGTHS if lengths else 0), _addr(q), _addr(q_out), _addr(kv), _addr(kv_out))
+    return q_out, kv_out
+
+
+class Rope:
+    """A model's rotary positions: the frequencies (rope_frequencies' arguments)
+    and the pair layout, kept on the device.  `rope(positions, q, kv, ...)`."""
+
+    def __init__(self, rot_dim: int = HEAD_DIM, base: float = 10000.0, interleaved: bool = False, device="cuda", **scaling):
+        self.inv_freq, self.mscale = rope_frequencies(rot_dim, base, device=device, **scaling)
+        self.interleaved = interleaved
+
+    def __call__(self, positions, q=None, kv=None, **kw):
+        return rope(positions, self.inv_freq, q, kv, interleaved=self.interleaved, mscale=self.mscale, **kw)
+
+
+# --------------------------------------------------------------------------
+# the 8-bit block-scaled cache
+# --------------------------------------------------------------------------
+def _need_q8(code_pages, page_scales) -> int:
+    """The cache's checks; its format."""
+    if code_pages is None or code_pages.dtype not in (torch.int8, torch.uint8):
+        raise TypeError("code_pages must be torch.int8 (INT8) or torch.uint8 (E4M3 codes)")
+    _need(code_pages, code_pages.dtype, "code_pages", 5)
+    _need(page_scales, torch.float32, "page_scales", 3)
+    NP, Hkv, two, P, D = code_pages.shape
+    if two != 2:
+        raise ValueError(f"code_pages must be [NP][Hkv][2][P][D], got {tuple(code_pages.shape)}")
+    _shape(page_scales, (NP, Hkv, 2), "page_scales")
+    return _lib.Q8_INT8 if code_pages.dtype == torch.int8 else _lib.Q8_E4M3
+
+
+def _need_requests(block_table, seq_lens, cu_tokens=None):
+    _need(block_table, torch.int32, "block_table", 2)
+    _need(seq_lens, torch.int32, "seq_lens", 1)
+    if block_table.shape[0] != seq_lens.shape[0]:
+        raise ValueError("block_table and seq_lens must have one row per request")
+    if cu_tokens is not None:
+        _need(cu_tokens, torch.int32, "cu_tokens", 1)
+        if cu_tokens.shape[0] != seq_lens.shape[0] + 1:
+            raise ValueError("cu_tokens must have one entry more than seq_lens")
+
+
+def new_q8_cache(num_pages: int, num_kv_heads: int, e4m3: bool = False, device="cuda"):
+    """(code_pages, page_scales) of an empty 8-bit cache."""
+    return (torch.zeros((num_pages, num_kv_heads, 2, PAGE, HEAD_DIM), dtype=torch.uint8 if e4m3 else torch.int8,
+                        device=device),
+            torch.zeros((num_pages, num_kv_heads, 2), dtype=torch.float32, device=device))
+
+
+def _q8_cache_call(name, kv, code_pages, page_scales, block_table, seq_lens, cu_tokens, status):
+    fmt = _need_q8(code_pages, page_scales)
+    _need(kv, torch.float16, "kv", 4)
+    _need_requests(block_table, seq_lens, cu_tokens)
+    NP, Hkv, _, P, D = code_pages.shape
+    T, B = kv.shape[0], seq_lens.shape[0]
+    _shape(kv, (T, Hkv, 2, D), "kv")
+    if cu_tokens is None and T != B:
+        raise ValueError("kv holds one token per request unless cu_tokens is given")
+    dev = _same_device(kv, code_pages=code_pages, page_scales=page_scales, block_table=block_table,
+                       seq_lens=seq_lens, cu_tokens=cu_tokens, status=status)
+    _launch(dev, name, _cfg_ref(D, P), fmt, B, T, Hkv, kv.data_ptr(), code_pages.data_ptr(), page_scales.data_ptr(),
+            NP, block_table.data_ptr(), block_table.shape[1], seq_lens.data_ptr(), _addr(cu_tokens), _addr(status))
+
+
+def q8_append(kv: torch.Tensor, code_pages: torch.Tensor, page_scales: torch.Tensor, block_table: torch.Tensor,
+              seq_lens: torch.Tensor, cu_tokens: torch.Tensor | None = None,
+              status: torch.Tensor | None = None) -> None:
+    """Append kv [T][Hkv][2][D] fp16 to the 8-bit cache code_pages
+    [NP][Hkv][2][P][D] (int8, or uint8 E4M3 codes) with page_scales [NP][Hkv][2]
+    fp32, in place: rows cu_tokens[b] .. cu_tokens[b + 1] - 1 are request b's last
+    tokens, ending at position seq_lens[b] - 1 (one per request without
+    cu_tokens)."""
+    _q8_cache_call("aq_q8_append", kv, code_pages, page_scales, block_table, seq_lens, cu_tokens, status)
+
+
+def q8_load(code_pages: torch.Tensor, page_scales: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
+            cu_tokens: torch.Tensor | None = None, num_tokens: int | None = None,
+            kv_out: torch.Tensor | None = None, status: torch.Tensor | None = None) -> torch.Tensor:
+    """Read tokens back from the 8-bit cache as fp16 [T][Hkv][2][D]: each
+    request's last cu_tokens[b + 1] - cu_tokens[b] tokens (its last one without
+    cu_tokens).  num_tokens (T) is needed with cu_tokens unless kv_out is given."""
+    if kv_out is None:
+        if num_tokens is None:
+            if cu_tokens is not None:
+                raise ValueError("num_tokens is required with cu_tokens")
+            num_tokens = seq_lens.shape[0]
+        kv_out = torch.empty((num_tokens, code_pages.shape[1], 2, code_pages.shape[4]), dtype=torch.float16,
+                             device=code_pages.device)
+    _q8_cache_call("aq_q8_load", kv_out, code_pages, page_scales, block_table, seq_lens, cu_tokens, status)
+    return kv_out
+
+
+@functools.lru_cache(maxsize=4096)
+def q8_decode_plan(batch: int, num_q_heads: int, num_kv_heads: int, max_seq_len: int, num_splits: int = 0):
+    """(num_splits, workspace_bytes) a q8_decode_attention call will use."""
+    s, w = ctypes.c_int32(), ctypes.c_size_t()
+    st = _lib.load().aq_q8_decode_plan(_cfg_ref(), batch, num_q_heads, num_kv_heads, max_seq_len, num_splits,
+                                       ctypes.byref(s), ctypes.byref(w))
+    _lib.check(st, "aq_q8_decode_plan")
+    return s.value, w.value
+
+
+def q8_decode_attention(q: torch.Tensor, code_pages: torch.Tensor, page_scales: torch.Tensor,
+                        block_table: torch.Tensor, seq_lens: torch.Tensor, max_seq_len: int,
+                        scale: float | None = None, num_splits: int = 0, out: torch.Tensor | None = None,
+                        workspace: torch.Tensor | None = None, status: torch.Tensor | None = None) -> torch.Tensor:
+    """Decode attention over the 8-bit cache; q [B][Hq][D] fp32, returns out
+    [B][Hq][D] fp32.  Any number of query heads per kv head."""
+    _need(q, torch.float32, "q", 3)
+    fmt = _need_q8(code_pages, page_scales)
+    _need_requests(block_table, seq_lens)
+    B, Hq, D = q.shape
+    NP, Hkv, _, P, _ = code_pages.shape
+    if seq_lens.shape[0] != B or code_pages.shape[4] != D:
+        raise ValueError("q must be [B][Hq][D] with the requests and head_dim of the cache")
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _need(out, torch.float32, "out", 3)
+        _shape(out, q.shape, "out")
+    need = q8_decode_plan(B, Hq, Hkv, max_seq_len, num_splits)[1]
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    dev = _same_device(q, code_pages=code_pages, page_scales=page_scales, block_table=block_table, seq_lens=seq_lens,
+                       out=out, workspace=workspace, status=status)
+    _launch(dev, "aq_q8_decode_attention", _cfg_ref(D, P), fmt, B, Hq, Hkv, q.data_ptr(), code_pages.data_ptr(),
+            page_scales.data_ptr(), NP, block_table.data_ptr(), block_table.shape[1], seq_lens.data_ptr(), max_seq_len,
+            D ** -0.5 if scale is None else scale, num_splits, out.data_ptr(), _addr(workspace),
+            workspace.numel() * workspace.element_size() if workspace is not None else 0, _addr(status))
+    return out
+
+
+# --------------------------------------------------------------------------
+# pages
+# --------------------------------------------------------------------------
+def _need_table(block_table, seq_lens, refcount):
+    _need_requests(block_table, seq_lens)
+    _need(refcount, torch.int32, "refcount", 1)
+    return block_table.shape[0], block_table.shape[1], refcount.shape[0]
+
+
+def _need_rows(rows, other, name):
+    _need(rows, torch.int32, "rows", 1)
+    if other is not None:
+        _need(other, torch.int32, name, 1)
+        _shape(other, rows.shape, name)
+
+
+def _pool_array(pools, num_pages, dev):
+    """The pools as the library takes them."""
+    if len(pools) > _lib.MAX_POOLS:
+        raise ValueError(f"at most {_lib.MAX_POOLS} pools")
+    arr = (_lib.PagePool * len(pools))()
+    for i, t in enumerate(pools):
+        if not t.is_cuda or not t.is_contiguous() or t.dim() < 2 or t.shape[0] != num_pages:
+            raise ValueError(f"pool {i} must be a contiguous CUDA tensor of {num_pages} pages")
+        if t.get_device() != dev:
+            raise ValueError(f"pool {i} is on {t.device}, the call's other tensors on device {dev}")
+        arr[i].data = t.data_ptr()
+        arr[i].page_bytes = t.stride(0) * t.element_size()
+    return arr
+
+
+@functools.lru_cache(maxsize=1024)
+def pages_workspace_bytes(num_rows: int, num_pages: int) -> int:
+    """Workspace of the page calls over a table of num_rows rows and num_pages pages."""
+    w = ctypes.c_size_t()
+    _lib.check(_lib.load().aq_pages_workspace(num_rows, num_pages, ctypes.byref(w)), "aq_pages_workspace")
+    return w.value
+
+
+def _page_workspace(workspace, R, NP, device):
+    if workspace is None:
+        return torch.empty(pages_workspace_bytes(R, NP), dtype=torch.uint8, device=device)
+    return workspace
+
+
+def _bytes(t):
+    return t.numel() * t.element_size()
+
+
+def pages_extend(rows: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                 refcount: torch.Tensor, pools, workspace: torch.Tensor | None = None,
+                 status: torch.Tensor | None = None) -> None:
+    """Rows (int32 [n]) of the table grow to new_lens: pages are allocated, and a
+    shared, partly filled last page is copied (in every pool) before it is
+    written.  block_table [R][max_pages], seq_lens [R] and refcount [NP] change
+    in place; pools are the caches whose pages the table holds."""
+    _need_rows(rows, new_lens, "new_lens")
+    R, MP, NP = _need_table(block_table, seq_lens, refcount)
+    ws = _page_workspace(workspace, R, NP, rows.device)
+    dev = _same_device(rows, new_lens=new_lens, block_table=block_table, seq_lens=seq_lens, refcount=refcount,
+                       workspace=ws, status=status)
+    arr = pools if isinstance(pools, ctypes.Array) else _pool_array(pools, NP, dev)
+    _launch(dev, "aq_pages_extend", rows.shape[0], rows.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(), R, MP,
+            seq_lens.data_ptr(), refcount.data_ptr(), NP, arr, len(arr), ws.data_ptr(), _bytes(ws), _addr(status))
+
+
+def pages_fork(src_rows: torch.Tensor, dst_rows: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
+               refcount: torch.Tensor, workspace: torch.Tensor | None = None,
+               status: torch.Tensor | None = None) -> None:
+    """Empty rows dst_rows (int32 [n]) become copies of src_rows, sharing their pages."""
+    _need_rows(src_rows, dst_rows, "dst_rows")
+    R, MP, NP = _need_table(block_table, seq_lens, refcount)
+    ws = _page_workspace(workspace, R, NP, src_rows.device)
+    dev = _same_device(src_rows, dst_rows=dst_rows, block_table=block_table, seq_lens=seq_lens, refcount=refcount,
+                       workspace=ws, status=status)
+    _launch(dev, "aq_pages_fork", src_rows.shape[0], src_rows.data_ptr(), dst_rows.data_ptr(), block_table.data_ptr(),
+            R, MP, seq_lens.data_ptr(), refcount.data_ptr(), NP, ws.data_ptr(), _bytes(ws), _addr(status))
+
+
+def pages_free(rows: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor, refcount: torch.Tensor,
+               keep_lens: torch.Tensor | None = None, status: torch.Tensor | None = None) -> None:
+    """Rows (int32 [n]) keep their first keep_lens tokens (none by default); the
+    pages behind them are given up."""
+    _need_rows(rows, keep_lens, "keep_lens")
+    R, MP, NP = _need_table(block_table, seq_lens, refcount)
+    dev = _same_device(rows, keep_lens=keep_lens, block_table=block_table, seq_lens=seq_lens, refcount=refcount,
+                       status=status)
+    _launch(dev, "aq_pages_free", rows.shape[0], rows.data_ptr(), _addr(keep_lens), block_table.data_ptr(), R, MP,
+            seq_lens.data_ptr(), refcount.data_ptr(), NP, _addr(status))
+
+
+def pages_compact(block_table: torch.Tensor, seq_lens: torch.Tensor, refcount: torch.Tensor, pools,
+                  workspace: torch.Tensor | None = None, status: torch.Tensor | None = None) -> None:
+    """Live pages move to the lowest ids (in every pool); the table follows."""
+    R, MP, NP = _need_table(block_table, seq_lens, refcount)
+    ws = _page_workspace(workspace, R, NP, refcount.device)
+    dev = _same_device(block_table, seq_lens=seq_lens, refcount=refcount, workspace=ws, status=status)
+    arr = pools if isinstance(pools, ctypes.Array) else _pool_array(pools, NP, dev)
+    _launch(dev, "aq_pages_compact", block_table.data_ptr(), R, MP, seq_lens.data_ptr(), refcount.data_ptr(), NP, arr,
+            len(arr), ws.data_ptr(), _bytes(ws), _addr(status))
+
+
+class PageTable:
+    """A block table over the pages of some caches: `pools` are tensors of
+    num_pages pages each (every layer's code_pages, page_scales, fp16 pages ...).
+    Holds block_table, seq_lens, refcount, a workspace and a status word; the
+    methods take int32 device tensors of rows."""
+
+    def __init__(self, num_rows: int, max_pages: int, pools):
+        self.pools = list(pools)
+        if not self.pools:
+            raise ValueError("at least one pool")
+        dev, num_pages = self.pools[0].device, int(self.pools[0].shape[0])
+        self._arr = _pool_array(self.pools, num_pages, self.pools[0].get_device())
+        self.block_table = torch.full((num_rows, max_pages), -1, dtype=torch.int32, device=dev)
+        self.seq_lens = torch.zeros(num_rows, dtype=torch.int32, device=dev)
+        self.refcount = torch.zeros(num_pages, dtype=torch.int32, device=dev)
+        self.workspace = torch.empty(pages_workspace_bytes(num_rows, num_pages), dtype=torch.uint8, device=dev)
+        self.status = new_status(dev)
+
+    def _state(self):
+        return self.block_table, self.seq_lens, self.refcount
+
+    def extend(self, rows, new_lens):
+        pages_extend(rows, new_lens, *self._state(), self._arr, self.workspace, self.status)
+
+    def fork(self, src_rows, dst_rows):
+        pages_fork(src_rows, dst_rows, *self._state(), self.workspace, self.status)
+
+    def free(self, rows, keep_lens=None):
+        pages_free(rows, *self._state(), keep_lens, self.status)
+
+    def compact(self):
+        pages_compact(*self._state(), self._arr, self.workspace, self.status)
+
+    def check_status(self):
+        """Raise if a call flagged a data error (reads the status word)."""
+        st = int(self.status.item())
+        if st:
+            raise RuntimeError(f"device status {st:#x}")
+
+
+class Q8DecodeStep:
+    """One decode step of a fixed batch over the 8-bit cache: the rotary
+    positions (with a Rope), the append of each request's current token (at
+    position seq_len - 1) and decode attention over all its tokens.  Holds the
+    cache tensors, workspace, output and a status word; `run(q, new_kv)` works on
+    the current stream and can be captured into a graph."""
+
+    def __init__(self, code_pages, page_scales, block_table, seq_lens, max_seq_len, num_q_heads, scale=None,
+                 num_splits=0, rope=None):
+        _need_q8(code_pages, page_scales)
+        self.code_pages, self.page_scales = code_pages, page_scales
+        self.block_table, self.seq_lens = block_table, seq_lens
+        self.max_seq_len, self.scale, self.num_splits = int(max_seq_len), scale, num_splits
+        B, Hkv, dev = int(seq_lens.shape[0]), int(code_pages.shape[1]), code_pages.device
+        need = q8_decode_plan(B, int(num_q_heads), Hkv, self.max_seq_len, num_splits)[1]
+        self.workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        self.status = new_status(dev)
+        self.out = torch.empty((B, int(num_q_heads), HEAD_DIM), dtype=torch.float32, device=dev)
+        self.rope = rope
+        if rope is not None:
+            self._q = torch.empty_like(self.out)
+            self._kv = torch.empty((B, Hkv, 2, HEAD_DIM), dtype=torch.float16, device=dev)
+
+    def run(self, q, new_kv, out=None):
+        if self.rope is not None:
+            q, new_kv = self.rope(self.seq_lens, q, new_kv, lengths=True, q_out=self._q, kv_out=self._kv)
+        q8_append(new_kv, self.code_pages, self.page_scales, self.block_table, self.seq_lens, status=self.status)
+        return q8_decode_attention(q, self.code_pages, self.page_scales, self.block_table, self.seq_lens,
+                                   self.max_seq_len, self.scale, self.num_splits,
+                                   out=self.out if out is None else out, workspace=self.workspace, status=self.status)
+
+    def check_status(self):
+        """Raise if a kernel flagged a data error (reads the status word)."""
+        st = int(self.status.item())
+        if st:
+            raise RuntimeError(f"device status {st:#x}")
+
+
 class DecodeStep:
     """One decode step of a fixed batch: append each request's current K/V
     token (the one at position seq_len-1) into the PQ code cache, then PQ
@@ -348,11 +757,12 @@ class DecodeStep:
     buffers can launch step i before it waits for step i-1's output (the copies
     and the kernel of one step overlap the host's work on the other).
     `overlap=True` launches the step as a programmatic dependent of the
-    preceding kernel (aq_decode_step's AQ_STEP_OVERLAP contract).
+    preceding kernel (aq_decode_step's AQ_STEP_OVERLAP contract).  With a Rope,
+    `run` first turns q and the new keys to position seq_len-1.
     """
 
     def __init__(self, code_pages, codebooks, req_set, block_table, seq_lens, max_seq_len,
-                 new_slot, new_set, num_q_heads, scale=None, num_splits=0, overlap=False):
+                 new_slot, new_set, num_q_heads, scale=None, num_splits=0, overlap=False, rope=None):
         self.code_pages, self.codebooks = code_pages, codebooks
         self.req_set, self.block_table, self.seq_lens = req_set, block_table, seq_lens
         self.max_seq_len = int(max_seq_len)
@@ -371,8 +781,14 @@ class DecodeStep:
         self._done = None
         self._io = None
         self.overlap = overlap
+        self.rope = rope
+        if rope is not None:
+            self._q = torch.empty_like(self.out)
+            self._kv = torch.empty((self.B, self.Hkv, 2, HEAD_DIM), dtype=torch.float16, device=dev)
 
     def run(self, q, new_kv, out=None):
+        if self.rope is not None:
+            q, new_kv = self.rope(self.seq_lens, q, new_kv, lengths=True, q_out=self._q, kv_out=self._kv)
         return decode_step(q, new_kv, self.code_pages, self.codebooks, self.req_set,
                            self.block_table, self.seq_lens, self.max_seq_len, self.scale,
                            self.num_splits, overlap=self.overlap, out=self.out if out is None else out,

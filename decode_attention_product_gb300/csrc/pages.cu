@@ -1,0 +1,550 @@
+// pages.cu -- the pages of a paged cache, managed on the device: rows of the
+// block table share pages (fork), grow (extend, copying a shared partial page
+// before it is written), shrink or end (free), and the pool is compacted.
+//
+// The only state beside the block table and seq_lens is refcount [NP]: page p
+// is free when refcount[p] == 0.  New pages are the lowest free ids, in the
+// order of the call's rows, so the result depends on nothing but the inputs:
+// there is no free list whose order could, and refcounts change by integer
+// atomics only.
+//
+// "The k-th free page" is a prefix count over refcount.  One launch counts
+// tiles of 4096 pages (and, in its first CTA, prefix-sums what each row needs);
+// the next gives every tile its rank base from the tile counts and hands its
+// free pages out; the last copies page data and publishes lengths.
+#include "common.cuh"
+#include "internal.h"
+
+namespace aq {
+
+namespace {
+
+constexpr int kThreads = 1024;
+constexpr int kTile = 4 * kThreads;
+constexpr int kMaxPools = 256;
+constexpr int kCopyThreads = 256;
+
+struct PageParams {
+    int32_t *block_table;          // [R][max_pages]
+    int32_t *seq_lens;             // [R]
+    int32_t *refcount;             // [NP]
+    const int32_t *rows, *args;    // [n]: extend: rows, new lengths; fork: sources, destinations; free: rows, kept lengths
+    int32_t *status;
+    // workspace
+    int32_t *tiles;                // [ntiles] pages counted per tile
+    int32_t *total;                // [4]: free or live pages, movers
+    long long *off;                // [R + 1] prefix of the rows' needs
+    int32_t *info;                 // [R]
+    int32_t *claim;                // [R]
+    int32_t *pair;                 // [R][2] page to copy from, to
+    int32_t *rank, *movers, *holes;    // [NP]
+    int32_t n, num_rows, max_pages, num_pages, ntiles, num_pools;
+};
+
+struct PagePools {
+    aq_page_pool pool[kMaxPools];
+};
+
+// Exclusive prefix of `v` over the block; *sum = the block's total.
+template <typename T>
+__device__ __forceinline__ T block_scan(T v, T *sum) {
+    __shared__ T part[kThreads / 32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    T x = v;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+        const T y = __shfl_up_sync(0xffffffffu, x, d);
+        if (lane >= d) x += y;
+    }
+    __syncthreads();                                   // part of an earlier call has been read
+    if (lane == 31) part[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+        T y = part[lane];
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const T z = __shfl_up_sync(0xffffffffu, y, d);
+            if (lane >= d) y += z;
+        }
+        part[lane] = y;
+    }
+    __syncthreads();
+    *sum = part[kThreads / 32 - 1];
+    return x - v + (warp ? part[warp - 1] : 0);
+}
+
+__device__ __forceinline__ bool row_ok(const PageParams &p, int row) { return row >= 0 && row < p.num_rows; }
+
+__device__ __forceinline__ bool len_ok(const PageParams &p, int len) {
+    return len >= 0 && len <= static_cast<int64_t>(p.max_pages) * kPage;
+}
+
+// The first of the call's entries that names a row owns it: claim[row] = the
+// lowest index.  Called by one CTA; entries outside [0, R) are left out.
+__device__ __forceinline__ void claim_rows(const PageParams &p, const int32_t *rows) {
+    for (int i = threadIdx.x; i < p.n; i += kThreads)
+        if (row_ok(p, rows[i])) p.claim[rows[i]] = 0x7fffffff;
+    __syncthreads();
+    for (int i = threadIdx.x; i < p.n; i += kThreads)
+        if (row_ok(p, rows[i])) atomicMin(&p.claim[rows[i]], i);
+    __syncthreads();
+}
+
+// Pages of tile `t`, four per thread; those outside the pool count as neither
+// free nor live (-1).
+__device__ __forceinline__ int4 tile_counts(const PageParams &p, int t) {
+    const int64_t i = static_cast<int64_t>(t) * kTile + 4 * threadIdx.x;
+    int4 r = make_int4(-1, -1, -1, -1);
+    if (i + 4 <= p.num_pages) r = *reinterpret_cast<const int4 *>(p.refcount + i);
+    else {
+        if (i < p.num_pages) r.x = p.refcount[i];
+        if (i + 1 < p.num_pages) r.y = p.refcount[i + 1];
+        if (i + 2 < p.num_pages) r.z = p.refcount[i + 2];
+    }
+    return r;
+}
+
+// What row entry i of an extend needs; info[i] = 1: its shared partial page is
+// copied first, -1: a data error, the row stays as it is.
+__device__ __forceinline__ int extend_need(const PageParams &p, int i) {
+    p.info[i] = -1;
+    p.pair[2 * i] = -1;
+    const int row = p.rows[i], len = p.args[i];
+    if (!row_ok(p, row) || __ldcg(&p.claim[row]) != i) {
+        flag_status(p.status, AQ_DEV_BAD_ROW);
+        return 0;
+    }
+    const int L = p.seq_lens[row];
+    if (!len_ok(p, L) || !len_ok(p, len) || len < L) {
+        flag_status(p.status, AQ_DEV_BAD_LENGTH);
+        return 0;
+    }
+    const int have = (L + kPage - 1) / kPage, want = (len - 1) / kPage + 1;
+    int copy = 0;
+    if (len > L && L % kPage) {
+        const int pg = p.block_table[static_cast<size_t>(row) * p.max_pages + have - 1];
+        if (pg < 0 || pg >= p.num_pages) {
+            flag_status(p.status, AQ_DEV_BAD_PAGE);
+            return 0;
+        }
+        copy = p.refcount[pg] > 1;
+    }
+    p.info[i] = copy;
+    return len > L ? want - have + copy : 0;
+}
+
+// First launch.  CTA 0 (extend): needs and their prefix.  The others: one tile.
+template <bool EXTEND>
+__global__ void __launch_bounds__(kThreads) pages_count_kernel(const __grid_constant__ PageParams p) {
+    if (EXTEND && blockIdx.x == 0) {
+        claim_rows(p, p.rows);
+        long long base = 0;
+        for (int i0 = 0; i0 < p.n; i0 += kThreads) {
+            const int i = i0 + threadIdx.x;
+            long long sum;
+            const long long need = i < p.n ? extend_need(p, i) : 0;
+            const long long at = block_scan(need, &sum);
+            if (i < p.n) p.off[i] = base + at;
+            base += sum;
+        }
+        if (threadIdx.x == 0) p.off[p.n] = base;
+        return;
+    }
+    const int t = blockIdx.x - (EXTEND ? 1 : 0);
+    const int4 r = tile_counts(p, t);
+    const int n = EXTEND ? (r.x == 0) + (r.y == 0) + (r.z == 0) + (r.w == 0) : (r.x > 0) + (r.y > 0) + (r.z > 0) + (r.w > 0);
+    int sum;
+    block_scan(n, &sum);
+    if (threadIdx.x == 0) p.tiles[t] = sum;
+}
+
+// Sum of the tile counts before tile `t`, and of all of them.
+__device__ __forceinline__ int tiles_before(const PageParams &p, int t, int *total) {
+    int below = 0, all = 0;
+    for (int i = threadIdx.x; i < p.ntiles; i += kThreads) {
+        const int x = p.tiles[i];
+        all += x;
+        if (i < t) below += x;
+    }
+    int sum_below;
+    block_scan(below, &sum_below);
+    block_scan(all, total);
+    return sum_below;
+}
+
+// Second launch of an extend: the tile's free pages go to the rows by rank.
+__global__ void __launch_bounds__(kThreads) pages_assign_kernel(const __grid_constant__ PageParams p) {
+    int total;
+    const int base = tiles_before(p, blockIdx.x, &total);
+    if (blockIdx.x == 0 && threadIdx.x == 0) p.total[0] = total;
+    const int4 r = tile_counts(p, blockIdx.x);
+    const int f[4] = {r.x == 0, r.y == 0, r.z == 0, r.w == 0};
+    int sum;
+    int rank = base + block_scan(f[0] + f[1] + f[2] + f[3], &sum);
+    const long long need = p.off[p.n];
+    for (int k = 0; k < 4; ++k) {
+        if (!f[k]) continue;
+        const int mine = rank++;
+        if (mine >= need) return;
+        int lo = 0, hi = p.n;                          // the last entry with off <= mine
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            if (p.off[mid] <= mine) lo = mid;
+            else hi = mid;
+        }
+        if (p.off[lo + 1] > total) continue;           // this row cannot be served: its pages stay free
+        const int pg = blockIdx.x * kTile + 4 * threadIdx.x + k;
+        const int row = p.rows[lo], copy = p.info[lo], j = static_cast<int>(mine - p.off[lo]);
+        int32_t *bt = p.block_table + static_cast<size_t>(row) * p.max_pages + (p.seq_lens[row] + kPage - 1) / kPage - copy + j;
+        if (copy && j == 0) {
+            p.pair[2 * lo] = *bt;
+            p.pair[2 * lo + 1] = pg;
+        }
+        *bt = pg;
+        p.refcount[pg] = 1;
+    }
+}
+
+// One page of every pool, this CTA's part of `parts`.
+__device__ __forceinline__ void copy_page(const PagePools &pools, int num_pools, int from, int to, int part, int parts) {
+    const int step = parts * blockDim.x, first = part * blockDim.x + threadIdx.x;
+    for (int k = 0; k < num_pools; ++k) {
+        const int64_t bytes = pools.pool[k].page_bytes;
+        unsigned char *data = static_cast<unsigned char *>(pools.pool[k].data);
+        if (bytes % 16 == 0) {
+            const uint4 *s = reinterpret_cast<const uint4 *>(data + from * bytes);
+            uint4 *d = reinterpret_cast<uint4 *>(data + to * bytes);
+            for (int64_t i = first; i < bytes / 16; i += step) d[i] = s[i];
+        } else {
+            const uint32_t *s = reinterpret_cast<const uint32_t *>(data + from * bytes);
+            uint32_t *d = reinterpret_cast<uint32_t *>(data + to * bytes);
+            for (int64_t i = first; i < bytes / 4; i += step) d[i] = s[i];
+        }
+    }
+}
+
+// Last launch of an extend: shared partial pages are copied, the copies' old
+// references dropped and the new lengths published.
+__global__ void __launch_bounds__(kCopyThreads) pages_grow_kernel(const __grid_constant__ PageParams p,
+                                                                  const __grid_constant__ PagePools pools) {
+    const int i = blockIdx.x;
+    if (p.info[i] < 0) return;
+    const bool served = p.off[i + 1] <= p.total[0];
+    if (blockIdx.y == 0 && threadIdx.x == 0) {
+        if (served) p.seq_lens[p.rows[i]] = p.args[i];
+        else flag_status(p.status, AQ_DEV_NO_PAGE);
+    }
+    const int from = p.pair[2 * i];
+    if (!served || from < 0) return;
+    if (blockIdx.y == 0 && threadIdx.x == 0) atomicSub(&p.refcount[from], 1);
+    copy_page(pools, p.num_pools, from, p.pair[2 * i + 1], blockIdx.y, gridDim.y);
+}
+
+// Fork: which entries hold (the destination is an empty row, named once).
+__global__ void __launch_bounds__(kThreads) pages_fork_check_kernel(const __grid_constant__ PageParams p) {
+    claim_rows(p, p.args);
+    for (int i = threadIdx.x; i < p.n; i += kThreads) {
+        const int src = p.rows[i], dst = p.args[i];
+        int L = -1;
+        if (!row_ok(p, src) || !row_ok(p, dst) || __ldcg(&p.claim[dst]) != i || p.seq_lens[dst] != 0)
+            flag_status(p.status, AQ_DEV_BAD_ROW);
+        else if (!len_ok(p, p.seq_lens[src])) flag_status(p.status, AQ_DEV_BAD_LENGTH);
+        else L = p.seq_lens[src];
+        p.info[i] = L;
+    }
+}
+
+__global__ void __launch_bounds__(kCopyThreads) pages_fork_kernel(const __grid_constant__ PageParams p) {
+    const int i = blockIdx.x, L = p.info[i];
+    if (L < 0) return;
+    const int32_t *src = p.block_table + static_cast<size_t>(p.rows[i]) * p.max_pages;
+    int32_t *dst = p.block_table + static_cast<size_t>(p.args[i]) * p.max_pages;
+    if (blockIdx.y == 0 && threadIdx.x == 0) p.seq_lens[p.args[i]] = L;
+    const int n = (L + kPage - 1) / kPage;
+    for (int j = blockIdx.y * kCopyThreads + threadIdx.x; j < n; j += gridDim.y * kCopyThreads) {
+        const int pg = src[j];
+        dst[j] = pg;
+        if (pg < 0 || pg >= p.num_pages || atomicAdd(&p.refcount[pg], 1) <= 0) flag_status(p.status, AQ_DEV_BAD_PAGE);
+    }
+}
+
+// Free: a row keeps its first `keep` tokens.  The atomic minimum makes a row
+// named twice lose each page once, whichever entry comes first.
+__global__ void __launch_bounds__(kCopyThreads) pages_free_kernel(const __grid_constant__ PageParams p) {
+    __shared__ int len;
+    const int row = p.rows[blockIdx.x], keep = p.args ? p.args[blockIdx.x] : 0;
+    if (threadIdx.x == 0) {
+        len = 0;
+        if (!row_ok(p, row)) flag_status(p.status, AQ_DEV_BAD_ROW);
+        else if (keep < 0 || !len_ok(p, *static_cast<volatile int32_t *>(p.seq_lens + row)))
+            flag_status(p.status, AQ_DEV_BAD_LENGTH);
+        else len = atomicMin(&p.seq_lens[row], keep);
+    }
+    __syncthreads();
+    const int n = (len + kPage - 1) / kPage;
+    for (int j = (max(keep, 0) + kPage - 1) / kPage + threadIdx.x; j < n; j += kCopyThreads) {
+        int32_t *e = p.block_table + static_cast<size_t>(row) * p.max_pages + j;
+        const int pg = *e;
+        *e = -1;
+        if (pg < 0 || pg >= p.num_pages) flag_status(p.status, AQ_DEV_BAD_PAGE);
+        else if (atomicSub(&p.refcount[pg], 1) <= 0) {
+            atomicAdd(&p.refcount[pg], 1);
+            flag_status(p.status, AQ_DEV_BAD_PAGE);
+        }
+    }
+}
+
+// Second launch of a compaction: with N live pages, live page p >= N is the
+// mover of rank (live pages in [N, p)), free page p < N the hole of rank (free
+// pages in [0, p)); there are as many movers as holes.
+__global__ void __launch_bounds__(kThreads) pages_map_kernel(const __grid_constant__ PageParams p) {
+    int live;
+    const int base = tiles_before(p, blockIdx.x, &live);
+    // live pages below N: whole tiles, and the part of the tile that holds N
+    int below;
+    const int cut = live / kTile;
+    int under = 0;
+    {
+        int dummy;
+        under = tiles_before(p, cut, &dummy);
+        if (cut < p.ntiles) {
+            const int4 r = tile_counts(p, cut);
+            const int i = cut * kTile + 4 * threadIdx.x;
+            const int n = (r.x > 0 && i < live) + (r.y > 0 && i + 1 < live) + (r.z > 0 && i + 2 < live) + (r.w > 0 && i + 3 < live);
+            block_scan(n, &below);
+            under += below;
+        }
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        p.total[0] = live;
+        p.total[1] = live - under;
+    }
+    const int4 r = tile_counts(p, blockIdx.x);
+    const int c[4] = {r.x, r.y, r.z, r.w};
+    int sum;
+    int before = base + block_scan((c[0] > 0) + (c[1] > 0) + (c[2] > 0) + (c[3] > 0), &sum);
+    for (int k = 0; k < 4; ++k) {
+        const int64_t pg = static_cast<int64_t>(blockIdx.x) * kTile + 4 * threadIdx.x + k;
+        if (pg >= p.num_pages) return;
+        int rank = -1;
+        if (c[k] > 0) {
+            if (pg >= live) {
+                rank = before - under;
+                p.movers[rank] = static_cast<int>(pg);
+            }
+            ++before;
+        } else if (pg < live) {
+            p.holes[pg - before] = static_cast<int>(pg);
+        }
+        p.rank[pg] = rank;
+    }
+}
+
+// Last launch of a compaction: movers are copied into holes and the block
+// table rewritten (the first `table_ctas` CTAs).
+__global__ void __launch_bounds__(kCopyThreads) pages_move_kernel(const __grid_constant__ PageParams p,
+                                                                  const __grid_constant__ PagePools pools,
+                                                                  int table_ctas, int parts) {
+    const int live = p.total[0], moves = p.total[1];
+    if (static_cast<int>(blockIdx.x) < table_ctas) {
+        for (int row = blockIdx.x; row < p.num_rows; row += table_ctas) {
+            const int L = p.seq_lens[row];
+            if (!len_ok(p, L)) {
+                if (threadIdx.x == 0) flag_status(p.status, AQ_DEV_BAD_LENGTH);
+                continue;
+            }
+            int32_t *bt = p.block_table + static_cast<size_t>(row) * p.max_pages;
+            for (int j = threadIdx.x; j < (L + kPage - 1) / kPage; j += kCopyThreads) {
+                const int pg = bt[j];
+                if (pg >= 0 && pg < live) continue;
+                const int rank = pg >= 0 && pg < p.num_pages ? p.rank[pg] : -1;
+                if (rank < 0) flag_status(p.status, AQ_DEV_BAD_PAGE);
+                else bt[j] = p.holes[rank];
+            }
+        }
+        return;
+    }
+    const int64_t units = static_cast<int64_t>(moves) * parts;
+    for (int64_t u = blockIdx.x - table_ctas; u < units; u += gridDim.x - table_ctas) {
+        const int64_t i = u / parts;
+        const int from = p.movers[i], to = p.holes[i];
+        if (u % parts == 0 && threadIdx.x == 0) {
+            p.refcount[to] = p.refcount[from];
+            p.refcount[from] = 0;
+        }
+        copy_page(pools, p.num_pools, from, to, static_cast<int>(u % parts), parts);
+    }
+}
+
+bool off16(const void *a) { return (reinterpret_cast<uintptr_t>(a) & 15u) != 0; }
+
+int tiles_of(int64_t pages) { return static_cast<int>((pages + kTile - 1) / kTile); }
+
+// Workspace: int32 arrays in this order, each from a 16-byte boundary.
+size_t ints(int64_t n) { return static_cast<size_t>((n + 3) / 4 * 4); }
+
+size_t workspace_ints(int32_t rows, int64_t pages) {
+    return ints(tiles_of(pages)) + 4 + ints(2 * (int64_t(rows) + 1)) + 2 * ints(rows) + ints(2 * int64_t(rows)) + 3 * ints(pages);
+}
+
+aq_status check_pages(int32_t n, int32_t num_rows, int32_t max_pages, int64_t num_pages) {
+    if (n < 0 || num_rows < 0 || max_pages < 0 || num_pages < 0) return AQ_ERR_INVALID_ARGUMENT;
+    if (num_pages > 0x7fff0000ll) return AQ_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(max_pages) * kPage > 0x7fffffffll) return AQ_ERR_UNSUPPORTED;
+    return AQ_OK;
+}
+
+aq_status check_pools(const aq_page_pool *pools, int32_t num_pools) {
+    if (num_pools < 0 || (num_pools > 0 && !pools)) return AQ_ERR_INVALID_ARGUMENT;
+    if (num_pools > kMaxPools) return AQ_ERR_UNSUPPORTED;
+    for (int k = 0; k < num_pools; ++k)
+        if (!pools[k].data || off16(pools[k].data) || pools[k].page_bytes < 4 || pools[k].page_bytes % 4)
+            return AQ_ERR_INVALID_ARGUMENT;
+    return AQ_OK;
+}
+
+PageParams page_params(int32_t n, const int32_t *rows, const int32_t *args, int32_t *block_table, int32_t num_rows,
+                       int32_t max_pages, int32_t *seq_lens, int32_t *refcount, int64_t num_pages, void *workspace,
+                       int32_t *status) {
+    PageParams p{};
+    p.block_table = block_table;
+    p.seq_lens = seq_lens;
+    p.refcount = refcount;
+    p.rows = rows;
+    p.args = args;
+    p.status = status;
+    p.n = n;
+    p.num_rows = num_rows;
+    p.max_pages = max_pages;
+    p.num_pages = static_cast<int32_t>(num_pages);
+    p.ntiles = tiles_of(num_pages);
+    int32_t *w = static_cast<int32_t *>(workspace);
+    if (w) {
+        p.tiles = w;
+        p.total = p.tiles + ints(p.ntiles);
+        p.off = reinterpret_cast<long long *>(p.total + 4);
+        p.info = p.total + 4 + ints(2 * (int64_t(num_rows) + 1));
+        p.claim = p.info + ints(num_rows);
+        p.pair = p.claim + ints(num_rows);
+        p.rank = p.pair + ints(2 * int64_t(num_rows));
+        p.movers = p.rank + ints(num_pages);
+        p.holes = p.movers + ints(num_pages);
+    }
+    return p;
+}
+
+// CTAs per page copy: 16 KiB each, 64 at most.
+int copy_parts(const PagePools &pools, int num_pools) {
+    int64_t bytes = 0;
+    for (int k = 0; k < num_pools; ++k) bytes = pools.pool[k].page_bytes > bytes ? pools.pool[k].page_bytes : bytes;
+    const int64_t parts = (bytes + 16383) / 16384;
+    return static_cast<int>(parts < 1 ? 1 : parts > 64 ? 64 : parts);
+}
+
+aq_status done() {
+    const cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess) return AQ_OK;
+    record_cuda_error(e);
+    return AQ_ERR_CUDA;
+}
+
+}  // namespace
+
+}  // namespace aq
+
+using namespace aq;
+
+extern "C" {
+
+aq_status aq_pages_workspace(int32_t num_rows, int64_t num_pages, size_t *workspace_bytes) {
+    const aq_status st = check_pages(0, num_rows, 0, num_pages);
+    if (st != AQ_OK) return st;
+    if (!workspace_bytes) return AQ_ERR_INVALID_ARGUMENT;
+    *workspace_bytes = workspace_ints(num_rows, num_pages) * sizeof(int32_t);
+    return AQ_OK;
+}
+
+aq_status aq_pages_extend(int32_t n, const int32_t *rows, const int32_t *new_lens, int32_t *block_table,
+                          int32_t num_rows, int32_t max_pages, int32_t *seq_lens, int32_t *refcount,
+                          int64_t num_pages, const aq_page_pool *pools, int32_t num_pools, void *workspace,
+                          size_t workspace_bytes, int32_t *device_status, aq_stream_t stream) {
+    aq_status st = check_pages(n, num_rows, max_pages, num_pages);
+    if (st == AQ_OK) st = check_pools(pools, num_pools);
+    if (st != AQ_OK) return st;
+    if (n == 0) return AQ_OK;
+    if (n > num_rows || !rows || !new_lens || !block_table || !seq_lens || (num_pages > 0 && !refcount) || off16(refcount))
+        return AQ_ERR_INVALID_ARGUMENT;
+    if (!workspace || workspace_bytes < workspace_ints(num_rows, num_pages) * sizeof(int32_t))
+        return AQ_ERR_WORKSPACE_TOO_SMALL;
+    if (off16(workspace)) return AQ_ERR_INVALID_ARGUMENT;
+    PageParams p = page_params(n, rows, new_lens, block_table, num_rows, max_pages, seq_lens, refcount, num_pages,
+                               workspace, device_status);
+    p.num_pools = num_pools;
+    PagePools pl{};
+    for (int k = 0; k < num_pools; ++k) pl.pool[k] = pools[k];
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    pages_count_kernel<true><<<p.ntiles + 1, kThreads, 0, s>>>(p);
+    pages_assign_kernel<<<p.ntiles > 0 ? p.ntiles : 1, kThreads, 0, s>>>(p);
+    pages_grow_kernel<<<dim3(n, copy_parts(pl, num_pools)), kCopyThreads, 0, s>>>(p, pl);
+    return done();
+}
+
+aq_status aq_pages_fork(int32_t n, const int32_t *src_rows, const int32_t *dst_rows, int32_t *block_table,
+                        int32_t num_rows, int32_t max_pages, int32_t *seq_lens, int32_t *refcount,
+                        int64_t num_pages, void *workspace, size_t workspace_bytes, int32_t *device_status,
+                        aq_stream_t stream) {
+    const aq_status st = check_pages(n, num_rows, max_pages, num_pages);
+    if (st != AQ_OK) return st;
+    if (n == 0) return AQ_OK;
+    if (n > num_rows || !src_rows || !dst_rows || !block_table || !seq_lens || (num_pages > 0 && !refcount) || off16(refcount))
+        return AQ_ERR_INVALID_ARGUMENT;
+    if (!workspace || workspace_bytes < workspace_ints(num_rows, num_pages) * sizeof(int32_t))
+        return AQ_ERR_WORKSPACE_TOO_SMALL;
+    if (off16(workspace)) return AQ_ERR_INVALID_ARGUMENT;
+    const PageParams p = page_params(n, src_rows, dst_rows, block_table, num_rows, max_pages, seq_lens, refcount,
+                                     num_pages, workspace, device_status);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    pages_fork_check_kernel<<<1, kThreads, 0, s>>>(p);
+    const int parts = (max_pages + 4 * kCopyThreads - 1) / (4 * kCopyThreads);
+    pages_fork_kernel<<<dim3(n, parts < 1 ? 1 : parts > 64 ? 64 : parts), kCopyThreads, 0, s>>>(p);
+    return done();
+}
+
+aq_status aq_pages_free(int32_t n, const int32_t *rows, const int32_t *keep_lens, int32_t *block_table,
+                        int32_t num_rows, int32_t max_pages, int32_t *seq_lens, int32_t *refcount,
+                        int64_t num_pages, int32_t *device_status, aq_stream_t stream) {
+    const aq_status st = check_pages(n, num_rows, max_pages, num_pages);
+    if (st != AQ_OK) return st;
+    if (n == 0) return AQ_OK;
+    if (!rows || !block_table || !seq_lens || (num_pages > 0 && !refcount) || off16(refcount)) return AQ_ERR_INVALID_ARGUMENT;
+    const PageParams p = page_params(n, rows, keep_lens, block_table, num_rows, max_pages, seq_lens, refcount,
+                                     num_pages, nullptr, device_status);
+    pages_free_kernel<<<n, kCopyThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
+    return done();
+}
+
+aq_status aq_pages_compact(int32_t *block_table, int32_t num_rows, int32_t max_pages, int32_t *seq_lens,
+                           int32_t *refcount, int64_t num_pages, const aq_page_pool *pools, int32_t num_pools,
+                           void *workspace, size_t workspace_bytes, int32_t *device_status, aq_stream_t stream) {
+    aq_status st = check_pages(0, num_rows, max_pages, num_pages);
+    if (st == AQ_OK) st = check_pools(pools, num_pools);
+    if (st != AQ_OK) return st;
+    if (num_pages == 0) return AQ_OK;
+    if (!refcount || off16(refcount) || (num_rows > 0 && (!block_table || !seq_lens))) return AQ_ERR_INVALID_ARGUMENT;
+    if (!workspace || workspace_bytes < workspace_ints(num_rows, num_pages) * sizeof(int32_t))
+        return AQ_ERR_WORKSPACE_TOO_SMALL;
+    if (off16(workspace)) return AQ_ERR_INVALID_ARGUMENT;
+    PageParams p = page_params(0, nullptr, nullptr, block_table, num_rows, max_pages, seq_lens, refcount, num_pages,
+                               workspace, device_status);
+    p.num_pools = num_pools;
+    PagePools pl{};
+    for (int k = 0; k < num_pools; ++k) pl.pool[k] = pools[k];
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    pages_count_kernel<false><<<p.ntiles, kThreads, 0, s>>>(p);
+    pages_map_kernel<<<p.ntiles, kThreads, 0, s>>>(p);
+    const int table = num_rows < 152 ? num_rows : 152;
+    pages_move_kernel<<<table + 152 * 6, kCopyThreads, 0, s>>>(p, pl, table, copy_parts(pl, num_pools));
+    return done();
+}
+
+}  // extern "C"

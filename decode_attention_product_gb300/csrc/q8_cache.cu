@@ -1,0 +1,244 @@
+// q8_cache.cu -- the 8-bit block-scaled cache: append of new tokens and the
+// read-back of cached ones.
+//
+// Work is cut by block: one warp per (request, page, kv head, K or V), so a
+// block's scale and its up to 16 rows belong to one warp and nothing is shared
+// between warps.  Lane l holds dims [4l, 4l + 4) of every row: 8-byte fp16
+// loads, 4-byte code stores, whole 128-byte lines per row.
+//
+// A ragged call knows its requests only on the device (cu_tokens).  Request b
+// owns the work units from v_b = cu_tokens[b] / 16 + 2 b on: appending n tokens
+// touches at most n / 16 + 2 pages, which v_{b+1} - v_b never undercuts, so the
+// host can size the grid from the token count alone (T / 16 + 2 B + 1 units,
+// two idle ones per request at most) and a warp finds its request by a 32-way
+// search over v.
+#include "common.cuh"
+#include "internal.h"
+#include "q8_common.cuh"
+
+namespace aq {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+
+struct Q8CacheParams {
+    __half *kv;                    // [T][Hkv][2][D]: read by the append, written by the read-back
+    uint8_t *pages;                // [NP][Hkv][2][P][D]
+    float *scales;                 // [NP][Hkv][2]
+    const int32_t *block_table;    // [B][max_pages]
+    const int32_t *seq_lens;       // [B]
+    const int32_t *cu_tokens;      // [B + 1], or null: one token per request
+    int32_t *status;
+    int64_t num_pages;
+    int32_t batch, num_tokens, num_kv_heads, max_pages;
+};
+
+struct Unit {
+    int page;                      // page id, -1: nothing to do
+    int s0, s1;                    // slots [s0, s1) of the page
+    int64_t row;                   // token row of slot s0
+};
+
+// The unit's block range, or page -1; data errors go to the status word and,
+// where `bad` is given, are reported with the rows they concern.
+__device__ __forceinline__ Unit find_unit(const Q8CacheParams &p, int u, int lane, bool *bad) {
+    constexpr int P = kPage;
+    Unit w{-1, 0, 0, 0};
+    int b = u, first = u, n = 1, local = 0;
+    if (p.cu_tokens) {
+        int lo = 0, hi = p.batch;
+        while (hi - lo > 1) {
+            const int step = (hi - lo + 31) / 32;
+            const int i = lo + lane * step;
+            const bool le = i < hi && p.cu_tokens[i] / P + 2 * i <= u;
+            const unsigned m = __ballot_sync(0xffffffffu, le);
+            const int k = m ? 31 - __clz(static_cast<int>(m)) : 0;
+            lo += k * step;
+            hi = min(hi, lo + step);
+        }
+        b = lo;
+        first = p.cu_tokens[b];
+        const int end = p.cu_tokens[b + 1];
+        local = u - (first / P + 2 * b);
+        if (first < 0 || end < first || end > p.num_tokens) {
+            if (lane == 0) flag_status(p.status, AQ_DEV_BAD_LENGTH);
+            return w;
+        }
+        n = end - first;
+        if (n == 0 || local < 0) return w;
+    }
+    const int L = p.seq_lens[b];
+    const int64_t start = static_cast<int64_t>(L) - n;
+    const bool long_ = L < 0 || start < 0 || L > static_cast<int64_t>(p.max_pages) * P;
+    const int p0 = long_ ? 0 : static_cast<int>(start / P);
+    const int np = long_ ? (n + P - 1) / P : (L - 1) / P + 1 - p0;
+    if (local >= np) return w;
+    if (long_) {                                       // no place in the cache: its rows in pieces of 16
+        if (lane == 0) flag_status(p.status, AQ_DEV_BAD_LENGTH);
+        w.s1 = min(P, n - local * P);
+        w.row = first + static_cast<int64_t>(local) * P;
+        if (bad) *bad = true;
+        return w;
+    }
+    const int64_t at = static_cast<int64_t>(p0 + local) * P;
+    w.s0 = static_cast<int>(max(start, at) - at);
+    w.s1 = static_cast<int>(min(static_cast<int64_t>(L) - at, static_cast<int64_t>(P)));
+    w.row = first + (at + w.s0 - start);
+    const int pg = p.block_table[static_cast<size_t>(b) * p.max_pages + p0 + local];
+    if (pg < 0 || pg >= p.num_pages) {
+        if (lane == 0) flag_status(p.status, AQ_DEV_BAD_PAGE);
+        if (bad) *bad = true;
+        return w;
+    }
+    w.page = pg;
+    return w;
+}
+
+template <int FMT>
+__global__ void __launch_bounds__(kThreads) q8_append_kernel(const __grid_constant__ Q8CacheParams p) {
+    constexpr int D = kHeadDim, P = kPage;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const Unit w = find_unit(p, blockIdx.x, lane, nullptr);
+    if (w.page < 0) return;
+    const int pairs = 2 * p.num_kv_heads;
+    for (int hp = blockIdx.y * kWarps + warp; hp < pairs; hp += gridDim.y * kWarps) {
+        const __half *src = p.kv + (static_cast<size_t>(w.row) * pairs + hp) * D + 4 * lane;
+        uint2 x[P];
+        uint32_t top = 0;                              // largest |half| bits of each 16-bit lane
+#pragma unroll
+        for (int s = 0; s < P; ++s) {
+            x[s] = make_uint2(0u, 0u);
+            if (s >= w.s0 && s < w.s1)
+                x[s] = ld_global_na_v2(src + static_cast<size_t>(s - w.s0) * pairs * D);
+        }
+#pragma unroll
+        for (int s = 0; s < P; ++s)
+            top = __vmaxu2(top, __vmaxu2(x[s].x & 0x7fff7fffu, x[s].y & 0x7fff7fffu));
+        top = max(top & 0xffffu, top >> 16);
+        top = __reduce_max_sync(0xffffffffu, top);
+        const size_t block = static_cast<size_t>(w.page) * pairs + hp;
+        const float old = w.s0 > 0 ? p.scales[block] : 0.f;
+        // a block that holds a non-finite value is NaN as a whole (codes 0)
+        const float want = top >= 0x7c00u ? __int_as_float(0x7fc00000)
+                                          : scale_for<FMT>(__half2float(__ushort_as_half(static_cast<unsigned short>(top))));
+        const float scale = old != old ? old : (want > old || want != want) ? want : old;
+        uint32_t *dst = reinterpret_cast<uint32_t *>(p.pages + block * (P * D)) + lane;
+        if (w.s0 > 0 && scale != old && old == old) {  // earlier tokens of the block, under the grown scale
+            for (int s = 0; s < w.s0; ++s) dst[s * (D / 4)] = rescale4<FMT>(dst[s * (D / 4)], old, scale);
+        }
+#pragma unroll
+        for (int s = 0; s < P; ++s) {
+            if (s >= w.s0 && s < w.s1) {
+                const float2 a = h2_to_f2(x[s].x), b = h2_to_f2(x[s].y);
+                dst[s * (D / 4)] = encode4<FMT>(make_float4(a.x, a.y, b.x, b.y), scale);
+            }
+        }
+        if (lane == 0 && (w.s0 == 0 || scale != old)) p.scales[block] = scale;
+    }
+}
+
+template <int FMT>
+__global__ void __launch_bounds__(kThreads) q8_load_kernel(const __grid_constant__ Q8CacheParams p) {
+    constexpr int D = kHeadDim, P = kPage;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    bool bad = false;
+    const Unit w = find_unit(p, blockIdx.x, lane, &bad);
+    if (w.page < 0 && !bad) return;
+    const int pairs = 2 * p.num_kv_heads;
+    for (int hp = blockIdx.y * kWarps + warp; hp < pairs; hp += gridDim.y * kWarps) {
+        __half *dst = p.kv + (static_cast<size_t>(w.row) * pairs + hp) * D + 4 * lane;
+        const size_t block = static_cast<size_t>(bad ? 0 : w.page) * pairs + hp;
+        const float scale = bad ? __int_as_float(0x7fc00000) : p.scales[block];
+        const uint32_t *src = reinterpret_cast<const uint32_t *>(p.pages + block * (P * D)) + lane;
+        uint32_t c[P];
+#pragma unroll
+        for (int s = 0; s < P; ++s) c[s] = !bad && s >= w.s0 && s < w.s1 ? src[s * (D / 4)] : 0u;
+#pragma unroll
+        for (int s = 0; s < P; ++s) {
+            if (s >= w.s0 && s < w.s1) {
+                uint32_t lo, hi;
+                widen4<FMT>(c[s], lo, hi);
+                const float2 a = h2_to_f2(lo), b = h2_to_f2(hi);
+                const __half2 l = __floats2half2_rn(a.x * scale, a.y * scale);
+                const __half2 h = __floats2half2_rn(b.x * scale, b.y * scale);
+                uint2 r;
+                r.x = *reinterpret_cast<const uint32_t *>(&l);
+                r.y = *reinterpret_cast<const uint32_t *>(&h);
+                *reinterpret_cast<uint2 *>(dst + static_cast<size_t>(s - w.s0) * pairs * D) = r;
+            }
+        }
+    }
+}
+
+aq_status q8_cache_call(bool append, const aq_pq_config *cfg, int32_t format, int32_t batch, int32_t num_tokens,
+                        int32_t num_kv_heads, const void *kv, void *code_pages, float *page_scales,
+                        int64_t num_pages, const int32_t *block_table, int32_t max_pages, const int32_t *seq_lens,
+                        const int32_t *cu_tokens, int32_t *device_status, aq_stream_t stream) {
+    if (!cfg || cfg->head_dim <= 0 || cfg->page_size <= 0) return AQ_ERR_INVALID_ARGUMENT;
+    if (cfg->head_dim != kHeadDim || cfg->page_size != kPage) return AQ_ERR_UNSUPPORTED;
+    if (format != AQ_Q8_INT8 && format != AQ_Q8_E4M3) return AQ_ERR_INVALID_ARGUMENT;
+    if (batch < 0 || num_tokens < 0 || num_kv_heads < 1 || num_pages < 0 || max_pages < 0) return AQ_ERR_INVALID_ARGUMENT;
+    if (!cu_tokens && num_tokens != batch) return AQ_ERR_INVALID_ARGUMENT;
+    if (num_kv_heads > 65535 || batch > 65535) return AQ_ERR_UNSUPPORTED;
+    if (batch == 0 || num_tokens == 0) return AQ_OK;
+    if (!kv || !code_pages || !page_scales || !block_table || !seq_lens) return AQ_ERR_INVALID_ARGUMENT;
+    auto off16 = [](const void *a) { return (reinterpret_cast<uintptr_t>(a) & 15u) != 0; };
+    if (off16(kv) || off16(code_pages) || off16(page_scales)) return AQ_ERR_INVALID_ARGUMENT;
+    Q8CacheParams p{};
+    p.kv = static_cast<__half *>(const_cast<void *>(kv));
+    p.pages = static_cast<uint8_t *>(code_pages);
+    p.scales = page_scales;
+    p.block_table = block_table;
+    p.seq_lens = seq_lens;
+    p.cu_tokens = cu_tokens;
+    p.status = device_status;
+    p.num_pages = num_pages;
+    p.batch = batch;
+    p.num_tokens = num_tokens;
+    p.num_kv_heads = num_kv_heads;
+    p.max_pages = max_pages;
+    const unsigned units = cu_tokens ? static_cast<unsigned>(num_tokens / kPage) + 2u * batch + 1u
+                                     : static_cast<unsigned>(batch);
+    const dim3 grid(units, static_cast<unsigned>((2 * num_kv_heads + kWarps - 1) / kWarps));
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (append) {
+        if (format == AQ_Q8_INT8) q8_append_kernel<kInt8><<<grid, kThreads, 0, s>>>(p);
+        else q8_append_kernel<kE4m3><<<grid, kThreads, 0, s>>>(p);
+    } else {
+        if (format == AQ_Q8_INT8) q8_load_kernel<kInt8><<<grid, kThreads, 0, s>>>(p);
+        else q8_load_kernel<kE4m3><<<grid, kThreads, 0, s>>>(p);
+    }
+    const cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess) return AQ_OK;
+    record_cuda_error(e);
+    return AQ_ERR_CUDA;
+}
+
+}  // namespace
+
+}  // namespace aq
+
+using namespace aq;
+
+extern "C" {
+
+aq_status aq_q8_append(const aq_pq_config *cfg, int32_t format, int32_t batch, int32_t num_tokens,
+                       int32_t num_kv_heads, const void *kv_f16, void *code_pages, float *page_scales,
+                       int64_t num_pages, const int32_t *block_table, int32_t max_pages, const int32_t *seq_lens,
+                       const int32_t *cu_tokens, int32_t *device_status, aq_stream_t stream) {
+    return q8_cache_call(true, cfg, format, batch, num_tokens, num_kv_heads, kv_f16, code_pages, page_scales,
+                         num_pages, block_table, max_pages, seq_lens, cu_tokens, device_status, stream);
+}
+
+aq_status aq_q8_load(const aq_pq_config *cfg, int32_t format, int32_t batch, int32_t num_tokens,
+                     int32_t num_kv_heads, void *kv_f16, const void *code_pages, const float *page_scales,
+                     int64_t num_pages, const int32_t *block_table, int32_t max_pages, const int32_t *seq_lens,
+                     const int32_t *cu_tokens, int32_t *device_status, aq_stream_t stream) {
+    return q8_cache_call(false, cfg, format, batch, num_tokens, num_kv_heads, kv_f16, const_cast<void *>(code_pages),
+                         const_cast<float *>(page_scales), num_pages, block_table, max_pages, seq_lens, cu_tokens,
+                         device_status, stream);
+}
+
+}  // extern "C"

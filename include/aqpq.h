@@ -76,6 +76,9 @@ typedef int32_t aq_status;
 #define AQ_DEV_TIMEOUT     8  /* an asynchronous copy did not land in time         */
 #define AQ_DEV_INVARIANT  16  /* builds with AQ_DEBUG_CHECKS only: an internal
                                  invariant of a kernel failed (never set otherwise) */
+#define AQ_DEV_NO_PAGE    32  /* an extend found too few free pages for a row      */
+#define AQ_DEV_BAD_ROW    64  /* a row outside the block table, named twice, or a
+                                 fork's destination that is not empty              */
 
 typedef struct CUstream_st *aq_stream_t;   /* == cudaStream_t */
 
@@ -465,6 +468,193 @@ aq_status aq_decode_attention_noalloc(const aq_pq_config *cfg, int32_t batch,
                                       const int32_t *seq_lens, int32_t max_seq_len,
                                       float scale, int32_t num_splits, float *out,
                                       int32_t *device_status, aq_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * aq_rope -- rotary positions of queries and new keys, ahead of an append or a
+ * decode step (on any of the caches).  The pages name no position encoding: it
+ * is what a model's attention layer applies before the cache.
+ *
+ * For every token t and head, each pair (x1, x2) of the first rot_dim dims turns
+ * by the angle a = positions[t] * inv_freq[pair]:
+ *   y1 = mscale * (x1 cos a - x2 sin a),  y2 = mscale * (x1 sin a + x2 cos a)
+ * Pair i is dims (i, i + rot_dim / 2), or (2 i, 2 i + 1) with
+ * AQ_ROPE_INTERLEAVED.  AQ_ROPE_TRANSPOSE negates the sines: the transposed
+ * map, i.e. the gradient (and, with 1 / mscale, the inverse).  Dims from rot_dim
+ * on, and values, pass through.  The angle is reduced exactly for any position;
+ * the arithmetic is fp32, keys are rounded to fp16 once.
+ *
+ *   positions  in   int32 [T]; a negative one marks padding: that token's rows
+ *                   pass through unturned.  With AQ_ROPE_LENGTHS positions holds
+ *                   sequence lengths and token t stands at positions[t] - 1
+ *                   (a decode step's current tokens)
+ *   inv_freq   in   double [rot_dim / 2] (device), from aq_rope_frequencies
+ *   q, q_out   fp32 [T][Hq][D], both or neither
+ *   kv, kv_out fp16 [T][Hkv][2][D], both or neither; keys turn
+ *   An output may be its input (in place: padding, values and unturned dims are
+ *   then not touched); other overlaps are not allowed.
+ * Requires rot_dim a multiple of 8 in [8, D].  Only cfg->head_dim is used.
+ * ------------------------------------------------------------------------- */
+#define AQ_ROPE_INTERLEAVED 1
+#define AQ_ROPE_TRANSPOSE   2
+#define AQ_ROPE_LENGTHS     4
+aq_status aq_rope(const aq_pq_config *cfg, int32_t num_tokens, int32_t num_q_heads,
+                  int32_t num_kv_heads, const int32_t *positions, const double *inv_freq,
+                  int32_t rot_dim, float mscale, int32_t flags, const float *q,
+                  float *q_out, const void *kv_f16, void *kv_out_f16,
+                  aq_stream_t stream);
+
+/* aq_rope_frequencies -- host-only: inv_freq [rot_dim / 2] (HOST doubles) and
+ * the magnitude mscale for aq_rope.  With w_i = base^(-2 i / rot_dim):
+ *   AQ_ROPE_PLAIN    w_i
+ *   AQ_ROPE_LINEAR   w_i / factor (positions squeezed into the old range)
+ *   AQ_ROPE_NTK      base * factor^(rot_dim / (rot_dim - 2)) in place of base
+ *   AQ_ROPE_YARN     w_i for pairs that turn more than beta_fast times over
+ *                    original_len tokens, w_i / factor for those that turn less
+ *                    than beta_slow times, a linear ramp between (pair indices
+ *                    floored and ceiled); mscale = 0.1 ln(factor) + 1
+ * mscale is 1 but for AQ_ROPE_YARN.  Requires base > 1, factor >= 1;
+ * original_len and the betas are used by AQ_ROPE_YARN only. */
+#define AQ_ROPE_PLAIN  0
+#define AQ_ROPE_LINEAR 1
+#define AQ_ROPE_NTK    2
+#define AQ_ROPE_YARN   3
+aq_status aq_rope_frequencies(int32_t rot_dim, double base, int32_t scaling, double factor,
+                              int32_t original_len, double beta_fast, double beta_slow,
+                              double *inv_freq, float *mscale);
+
+/* ---------------------------------------------------------------------------
+ * The 8-bit block-scaled cache: between the fp16 cache and the PQ one (half the
+ * fp16 bytes, no codebooks).  A block is one page of one kv head's keys or
+ * values; its 8-bit codes stand for code * scale, one fp32 scale per block.
+ *   code_pages   [NP][Hkv][2][P][D] int8 (AQ_Q8_INT8) or E4M3 codes (AQ_Q8_E4M3)
+ *   page_scales  fp32 [NP][Hkv][2]
+ *
+ * aq_q8_append -- append tokens to their requests.  Request b appends its
+ * n_b = cu_tokens[b + 1] - cu_tokens[b] tokens, rows cu_tokens[b] .. of kv_f16,
+ * at positions seq_lens[b] - n_b .. seq_lens[b] - 1 (one token per request with
+ * cu_tokens NULL).  For each block that the call touches, amax = the largest
+ * magnitude among the call's tokens of the block:
+ *   INT8  scale = max(old scale, fp32(amax / 127)),   code = nearest(x / scale)
+ *   E4M3  scale = max(old scale, the least power of two with amax <= 448 scale)
+ * (ties to even, of the real quotient).  The old scale counts when the block
+ * holds earlier tokens of the request, i.e. when its first new slot is not slot
+ * 0; where the scale grows their codes are rounded again under it.  A block
+ * whose magnitudes are all zero has scale 0; one that holds a non-finite value
+ * has scale NaN and codes 0, and stays so.  Slots behind the last token, and
+ * every other page, are left as they were.  Pages written must belong to one
+ * request of the call (aq_pages_extend sees to that).
+ *
+ *   kv_f16     in   fp16 [T][Hkv][2][D]
+ *   cu_tokens  in   int32 [B + 1], nondecreasing within [0, T], or NULL (T == B);
+ *                   rows from cu_tokens[B] on are not read
+ *   A request that does not fit (n_b > seq_lens[b], a length beyond the block
+ *   table, an inconsistent cu_tokens) sets AQ_DEV_BAD_LENGTH and appends
+ *   nothing; a bad page sets AQ_DEV_BAD_PAGE and is skipped.
+ *
+ * aq_q8_load -- the same tokens read back as fp16(code * scale) into the same
+ * [T][Hkv][2][D] layout: the last n_b tokens of each request (for the attention
+ * of a next prefill chunk, or for aq_encode_append into a PQ cache).  Rows of a
+ * request or page that does not fit become NaN.
+ * ------------------------------------------------------------------------- */
+#define AQ_Q8_INT8 0
+#define AQ_Q8_E4M3 1
+aq_status aq_q8_append(const aq_pq_config *cfg, int32_t format, int32_t batch,
+                       int32_t num_tokens, int32_t num_kv_heads, const void *kv_f16,
+                       void *code_pages, float *page_scales, int64_t num_pages,
+                       const int32_t *block_table, int32_t max_pages,
+                       const int32_t *seq_lens, const int32_t *cu_tokens,
+                       int32_t *device_status, aq_stream_t stream);
+aq_status aq_q8_load(const aq_pq_config *cfg, int32_t format, int32_t batch,
+                     int32_t num_tokens, int32_t num_kv_heads, void *kv_f16,
+                     const void *code_pages, const float *page_scales, int64_t num_pages,
+                     const int32_t *block_table, int32_t max_pages,
+                     const int32_t *seq_lens, const int32_t *cu_tokens,
+                     int32_t *device_status, aq_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * aq_q8_decode_attention -- aq_decode_attention over the 8-bit cache: softmax
+ * attention of one query per request over the values that its first seq_lens[b]
+ * tokens' codes stand for, any number of query heads per kv head (Hq a multiple
+ * of Hkv).  Lengths, errors, splits, workspace and out as there; scales are
+ * finite and >= 0, or NaN, which makes the outputs that read the block NaN.
+ * aq_q8_decode_plan gives the splits and the workspace a call uses (host only).
+ * ------------------------------------------------------------------------- */
+aq_status aq_q8_decode_plan(const aq_pq_config *cfg, int32_t batch, int32_t num_q_heads,
+                            int32_t num_kv_heads, int32_t max_seq_len,
+                            int32_t num_splits_req, int32_t *num_splits,
+                            size_t *workspace_bytes);
+aq_status aq_q8_decode_attention(const aq_pq_config *cfg, int32_t format, int32_t batch,
+                                 int32_t num_q_heads, int32_t num_kv_heads, const float *q,
+                                 const void *code_pages, const float *page_scales,
+                                 int64_t num_pages, const int32_t *block_table,
+                                 int32_t max_pages, const int32_t *seq_lens,
+                                 int32_t max_seq_len, float scale, int32_t num_splits,
+                                 float *out, void *workspace, size_t workspace_bytes,
+                                 int32_t *device_status, aq_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Page management, on the device, for any of the paged caches (PAM article
+ * §2.2.2: a global block table over a pool of pages).  Row r of the block table
+ * [R][max_pages] holds the pages of a request with seq_lens[r] tokens (0: an
+ * empty row): entries 0 .. ceil(seq_lens[r] / P) - 1 count, the others do not.
+ * refcount int32 [NP] is the number of rows that hold a page; 0 means free.  The
+ * calls change block_table, seq_lens and refcount in place; the caller starts
+ * from an empty table (all lengths and refcounts 0).  New pages are the lowest
+ * free ids, in the order of the call's rows.  Rows are device int32 arrays; each
+ * names rows of the table.  Entries that break a rule below set a status bit and
+ * change nothing; the others are carried out.
+ *   pools  host array of up to 256 caches whose pages move with the table's (all
+ *          layers' pools, and page_scales beside code_pages): data [NP] pages of
+ *          page_bytes each (a multiple of 4; base 16-byte aligned)
+ *   workspace  >= aq_pages_workspace() bytes, no initialisation needed
+ *
+ * aq_pages_extend  row rows[i] grows to new_lens[i] >= its length: missing pages
+ *                  are allocated, and a partly filled last page that other rows
+ *                  share is copied to a new one first (its tokens are about to
+ *                  be written).  seq_lens becomes new_lens[i]; the appended
+ *                  tokens' slots are not written.  A row named twice
+ *                  (AQ_DEV_BAD_ROW) counts once, by its first entry.  Rows are
+ *                  served in order: a row whose pages, with those of the rows
+ *                  before it, exceed the free ones sets AQ_DEV_NO_PAGE.
+ * aq_pages_fork    the empty row dst_rows[i] becomes a copy of src_rows[i],
+ *                  sharing all its pages.  A destination that is not empty, or
+ *                  named before, sets AQ_DEV_BAD_ROW.
+ * aq_pages_free    row rows[i] keeps its first keep_lens[i] tokens (none with
+ *                  keep_lens NULL; a longer length keeps all): pages behind them
+ *                  lose a reference, their entries become -1.  A row may be
+ *                  named more than once: the shortest length holds.
+ * aq_pages_compact live pages move to ids 0 .. N - 1 (those already there stay),
+ *                  the block table follows, refcounts move along: the pool's
+ *                  tail from N on is free.
+ * A page id outside the pool, or without references where one must be, sets
+ * AQ_DEV_BAD_PAGE; a length outside [0, max_pages * P], a shrinking extend or a
+ * negative keep sets AQ_DEV_BAD_LENGTH.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+    void *data;
+    int64_t page_bytes;
+} aq_page_pool;
+aq_status aq_pages_workspace(int32_t num_rows, int64_t num_pages, size_t *workspace_bytes);
+aq_status aq_pages_extend(int32_t n, const int32_t *rows, const int32_t *new_lens,
+                          int32_t *block_table, int32_t num_rows, int32_t max_pages,
+                          int32_t *seq_lens, int32_t *refcount, int64_t num_pages,
+                          const aq_page_pool *pools, int32_t num_pools, void *workspace,
+                          size_t workspace_bytes, int32_t *device_status,
+                          aq_stream_t stream);
+aq_status aq_pages_fork(int32_t n, const int32_t *src_rows, const int32_t *dst_rows,
+                        int32_t *block_table, int32_t num_rows, int32_t max_pages,
+                        int32_t *seq_lens, int32_t *refcount, int64_t num_pages,
+                        void *workspace, size_t workspace_bytes, int32_t *device_status,
+                        aq_stream_t stream);
+aq_status aq_pages_free(int32_t n, const int32_t *rows, const int32_t *keep_lens,
+                        int32_t *block_table, int32_t num_rows, int32_t max_pages,
+                        int32_t *seq_lens, int32_t *refcount, int64_t num_pages,
+                        int32_t *device_status, aq_stream_t stream);
+aq_status aq_pages_compact(int32_t *block_table, int32_t num_rows, int32_t max_pages,
+                           int32_t *seq_lens, int32_t *refcount, int64_t num_pages,
+                           const aq_page_pool *pools, int32_t num_pools, void *workspace,
+                           size_t workspace_bytes, int32_t *device_status,
+                           aq_stream_t stream);
 
 #ifdef __cplusplus
 }
