@@ -342,7 +342,7 @@ CASES = [
 
 @pytest.mark.parametrize("fmt", ["int8", "e4m3"])
 @pytest.mark.parametrize("case", CASES, ids=[f"B{c[0]}H{c[1]}G{c[2]}L{max(c[3])}" for c in CASES])
-@pytest.mark.parametrize("splits", [0, 1, 2, 7])
+@pytest.mark.parametrize("splits", [0, 1, 2, 7, 11])
 def test_attention_matches_reference(A, case, fmt, splits):
     B, Hkv, G, lens = case
     p = problem(np.random.default_rng(B * 1000 + G * 10 + len(fmt)), B, Hkv, G, lens, fmt)
@@ -359,7 +359,7 @@ def test_attention_planned_longer_than_the_requests(A, fmt):
     """max_seq_len far above the lengths: whole splits are empty."""
     p = problem(np.random.default_rng(5), 3, 2, 4, [40, 0, 3], fmt)
     p["bt"] = np.concatenate([p["bt"], np.full((3, 500), -7, np.int32)], 1)
-    for splits in (0, 13):
+    for splits in (0, 5, 13):
         got, st = attend(A, p, splits, most=8000)
         assert st == 0
         close(got, *reference(p))
@@ -438,7 +438,7 @@ def test_attention_nan_blocks_and_data_errors(A, splits):
 def test_attention_writes_only_its_outputs(A, fmt):
     p = problem(np.random.default_rng(10), 3, 2, 3, [200, 0, 77], fmt)
     n = p["q"].size
-    for splits in (1, 3):
+    for splits in (1, 3, 12):
         need = A.q8_decode_plan(3, 6, 2, 200, splits)[1]
         buf = torch.full((n + 2048,), 7.0, device="cuda")
         ws = torch.full((need + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
@@ -454,20 +454,20 @@ def test_attention_in_two_streams_and_graphs(A):
     equal the plain call."""
     p = problem(np.random.default_rng(14), 4, 4, 4, [900, 30, 500, 411], "int8")
     t = [dev(p[k]) for k in ("q", "pages", "scales", "bt", "lens")]
-    want = A.q8_decode_attention(*t, 900, num_splits=4)
+    want = A.q8_decode_attention(*t, 900, num_splits=12)
     streams, outs = [torch.cuda.Stream() for _ in range(2)], []
     for s in streams:
         s.wait_stream(torch.cuda.current_stream())
         with torch.cuda.stream(s):
-            outs.append([A.q8_decode_attention(*t, 900, num_splits=4) for _ in range(5)])
+            outs.append([A.q8_decode_attention(*t, 900, num_splits=12) for _ in range(5)])
     torch.cuda.synchronize()
     assert all(torch.equal(o, want) for x in outs for o in x)
     graphs, outs = [], [torch.zeros_like(want) for _ in range(2)]
     for o in outs:
         g = torch.cuda.CUDAGraph()
-        ws = torch.empty(A.q8_decode_plan(4, 16, 4, 900, 4)[1], dtype=torch.uint8, device="cuda")
+        ws = torch.empty(A.q8_decode_plan(4, 16, 4, 900, 12)[1], dtype=torch.uint8, device="cuda")
         with torch.cuda.graph(g):
-            A.q8_decode_attention(*t, 900, num_splits=4, out=o, workspace=ws)
+            A.q8_decode_attention(*t, 900, num_splits=12, out=o, workspace=ws)
         graphs.append((g, ws))
     for s, (g, _) in zip(streams, graphs):
         s.wait_stream(torch.cuda.current_stream())
@@ -517,5 +517,37 @@ def test_wrappers_refuse(A):
         A.q8_decode_attention(q[:, :3].contiguous(), pages, sc, bt, lens, 30)           # 3 heads over 2
     with pytest.raises(A._lib.AQError):
         A.q8_decode_attention(q, pages, sc, bt, lens, 10**6)                            # beyond the table
+    wide = torch.zeros(2, 20, dtype=torch.int32, device="cuda")
     with pytest.raises(A._lib.AQError):
-        A.q8_decode_attention(q, pages, sc, bt, lens, 30, num_splits=2, workspace=torch.zeros(64, device="cuda"))
+        A.q8_decode_attention(q, pages, sc, wide, lens, 300, num_splits=9, workspace=torch.zeros(64, device="cuda"))
+
+
+def test_attention_wait_limit(A):
+    """With no time to wait for its copies a call ends all the same: every output
+    is NaN or right, NaN only with the timeout bit, and the next call is right.
+    (A cold cache of 100 MB, so that copies queue behind one another.)"""
+    g = np.random.default_rng(17)
+    p = problem(g, 26, 8, 1, [0, 16] + [int(x) for x in g.integers(1500, 2001, 24)], "int8")
+    want, tol = reference(p)
+    lib = A._lib.load()
+    t = [dev(p[k]) for k in ("q", "pages", "scales", "bt", "lens")]
+    flush = torch.zeros(300 << 20, dtype=torch.uint8, device="cuda")
+    for splits in (1, 4, 12):
+        seen, st = 0, A.new_status()
+        for limit in (0, 0, 0, None):
+            flush += 1
+            st.zero_()
+            prev = lib.aq_set_wait_limit_ns(limit) if limit is not None else None
+            try:
+                got = A.q8_decode_attention(*t, int(p["lens"].max()), num_splits=splits, status=st)
+                torch.cuda.synchronize()
+            finally:
+                if prev is not None:
+                    lib.aq_set_wait_limit_ns(prev)
+            got, flag = got.cpu().numpy(), int(st.item())
+            assert flag in ((0, 8) if limit is not None else (0,))
+            bad = np.isnan(got)
+            assert np.array_equal(bad.any(-1), bad.all(-1)) and (flag == 8) == bool(bad.any())
+            close(got[~bad.any(-1)], want[~bad.any(-1)], tol[~bad.any(-1)])
+            seen |= flag
+        assert seen == 8, splits

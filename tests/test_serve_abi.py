@@ -118,8 +118,10 @@ def test_q8_attention_refusals(lib):
                 dict(scales=ODD), dict(out=ODD), dict(ws=ODD, wsb=1 << 20)):
         assert _attend(lib, **bad) == INV, bad
     assert _attend(lib, Bn=70000) == UNS and _attend(lib, Hq=70000, Hkv=70000) == UNS
-    assert _attend(lib, splits=3) == WS                 # forced splits need a workspace
-    assert _attend(lib, splits=3, ws=FAKE, wsb=64) == WS
+    # up to 8 splits merge in a cluster; more need a workspace
+    assert _attend(lib, mp=64, most=1000, splits=9) == WS
+    assert _attend(lib, mp=64, most=1000, splits=9, ws=FAKE, wsb=64) == WS
+    assert _attend(lib, NP=1 << 31) == UNS              # a page copy's coordinate
     assert _attend(lib, Bn=0, q=None) == 0
 
 
@@ -133,7 +135,7 @@ def test_q8_plans(lib):
     for Bn, Hq, Hkv, L in [(1, 2, 2, 512), (8, 64, 8, 1000), (4, 32, 32, 2048), (1, 32, 32, 131072),
                            (256, 32, 32, 4096), (1, 1, 1, 2**31 - 1), (65535, 8, 1, 100)]:
         s, w = plan(Bn, Hq, Hkv, L)
-        assert 1 <= s <= 4096 and w >= (Bn * Hq * s * 130 * 4 if s > 1 else 0)
+        assert 1 <= s <= 4096 and w == (Bn * Hq * s * 130 * 4 if s > 8 else 0)
 
 
 # ------------------------------------------------------------------ pages ----
