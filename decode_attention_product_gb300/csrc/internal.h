@@ -135,4 +135,27 @@ struct SmemAttr {
 // rest serves as L1) at that point.
 cudaError_t ensure_smem_attr(SmemAttr &a, const void *func, size_t need, int carveout_pct = -1);
 
+// Launch `kern` as a programmatic dependent of the stream's preceding kernel:
+// its launch overlaps that kernel's end.  The kernel calls griddepcontrol.wait
+// before it touches memory, so stream order is kept as with a plain launch, and
+// lets its own dependents start only after that wait.  `cluster` CTAs along x.
+template <typename... Params, typename... Args>
+cudaError_t launch_dependent(void (*kern)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, int cluster,
+                             const Args &...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 }  // namespace aq

@@ -40,10 +40,13 @@ namespace aq {
 namespace {
 
 constexpr int kWarps = 4;
+static_assert(kWarps == 4, "the warps' flags are read by name");
 constexpr int kThreads = 32 * kWarps;
 constexpr int kStages = 3;             // pages in a warp's ring
 constexpr int kGroup = 8;              // query heads of a tile
 constexpr int kMaxCluster = 8;
+constexpr int kQueryPitch = 80;        // words of a query's fp16 pairs: 4 groups of 16 + 4
+constexpr int kSumPitch = 132;         // floats between heads of a warp's sums
 constexpr int kPageBytes = 2 * kPage * kHeadDim;
 constexpr float kWeightTop = 32768.f;  // weights enter the fp16 product as p * 2^15
 constexpr size_t kRingBytes = static_cast<size_t>(kWarps) * kStages * kPageBytes + 1024;
@@ -65,12 +68,18 @@ struct Q8AttnParams {
 };
 
 // One page to shared memory, counted in bytes on `bar`.
-__device__ __forceinline__ void tma_page(void *dst, const CUtensorMap *map, int z, uint64_t *bar) {
+__device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap *map, int z, uint32_t bar) {
     asm volatile(
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %3}], [%4];" ::
-            "r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(z), "r"(smem_u32(bar))
+            "r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(z), "r"(bar)
         : "memory");
+}
+
+__device__ __forceinline__ uint4 lds_v4(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
 }
 
 // Transpose of an 8x8 fp16 tile held as (row lane / 4, columns 2 (lane % 4) + {0, 1}).
@@ -80,10 +89,20 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     return y;
 }
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ float2 ld_cluster_f32x2(uint32_t addr) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
     return v;
+}
+
+__device__ __forceinline__ int ld_cluster_s32(uint32_t addr) {
+    int v;
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void cluster_arrive_release() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
 
 __device__ __forceinline__ uint32_t word(const uint4 &v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
@@ -102,9 +121,13 @@ __global__ void __launch_bounds__(kThreads, 4) q8_attention_kernel(const __grid_
     extern __shared__ unsigned char ring_raw[];
     __shared__ uint64_t bars[kWarps][kStages];
     __shared__ float wm[kWarps][kGroup], wl[kWarps][kGroup];
-    __shared__ __align__(16) float co[kGroup][D];          // this CTA's sums, read by the cluster
-    __shared__ float cm[kGroup], cl[kGroup];
-    __shared__ int cbad;
+    // first the queries' fp16 parts (qw), then this CTA's sums, read by the cluster (co)
+    __shared__ __align__(16) uint32_t qw[2][kGroup][kQueryPitch];
+    __shared__ float qdown[kGroup];
+    float *co = reinterpret_cast<float *>(qw);
+    static_assert(sizeof(qw) >= sizeof(float) * kGroup * kHeadDim, "the sums take the queries' place");
+    __shared__ __align__(8) float2 cml[kGroup];
+    __shared__ int wbad[kWarps], cflag;
     // the ring starts on the swizzle's period
     unsigned char *ring = ring_raw + ((1024u - (smem_u32(ring_raw) & 1023u)) & 1023u);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -115,19 +138,31 @@ __global__ void __launch_bounds__(kThreads, 4) q8_attention_kernel(const __grid_
     const int S_ = p.num_splits;
     const float nan = __int_as_float(0x7fc00000);
 
-    // the request's pages, shared out evenly over its splits
-    const int L = p.seq_lens[b];
-    const bool badlen = L < 0 || L > static_cast<int64_t>(p.max_pages) * P || L > p.max_seq_len;
-    const int np = badlen ? 0 : (L + P - 1) / P;
-    const int pg0 = static_cast<int>(static_cast<int64_t>(np) * split / S_);
-    const int pg1 = static_cast<int>(static_cast<int64_t>(np) * (split + 1) / S_);
-    const int mine = pg1 - pg0 > warp ? (pg1 - pg0 - warp + kWarps - 1) / kWarps : 0;      // pg0 + warp, + kWarps, ...
-    const int32_t *bt = p.block_table + static_cast<size_t>(b) * p.max_pages + pg0 + warp;
-    unsigned char *stage = ring + static_cast<size_t>(warp) * kStages * kPageBytes;
-
+    if (lane == 0) {
+        for (int i = 0; i < kStages; ++i) mbar_init(&bars[warp][i], 1);
+        fence_mbar_init();
+    }
+    __syncwarp();
+    grid_dependency_wait();
+    grid_launch_dependents();
+    // Small loads go out before the page copies: behind those they would queue for
+    // microseconds (page1: all 512 CTAs' first copies take 3.5 us).  First the queries: 16 threads per head.
+    uint4 xq[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+    if (tid / 16 < heads) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) xq[j] = ld_global_na_v4(p.q + (bh0 + tid / 16) * D + 8 * (tid % 16) + 4 * j);
+    }
+    // page w0 + k * stride of the request is this warp's k-th: known before the length is,
+    // so the first ids and the length are fetched together
+    const int w0 = split * kWarps + warp, stride = S_ * kWarps;
+    const int32_t *bt = p.block_table + static_cast<size_t>(b) * p.max_pages;
+    const uint32_t stage = smem_u32(ring) + warp * kStages * kPageBytes, bar0 = smem_u32(&bars[warp][0]);
+    // this lane's first 16-byte chunks of keys (row r, chunk 2 c) and values (row 2 c, chunk r)
+    const uint32_t at_k = r * D + (((2 * c) ^ r) << 4), at_v = (P + 2 * c) * D + ((r ^ (2 * c)) << 4);
     // page ids (-1: outside the pool) and scales of the warp's pages [k, k + 32), one per lane
     auto page_id = [&](int k) {
-        const int pg = k < mine ? bt[static_cast<size_t>(k) * kWarps] : -1;
+        const int64_t i = w0 + static_cast<int64_t>(k) * stride;
+        const int pg = i < p.max_pages ? bt[i] : -1;
         return pg >= 0 && pg < p.num_pages ? pg : -1;
     };
     auto page_scales = [&](int pg) {
@@ -135,105 +170,118 @@ __global__ void __launch_bounds__(kThreads, 4) q8_attention_kernel(const __grid_
                        : make_float2(0.f, 0.f);
     };
     int id = page_id(lane);
-    if (tid == 0) cbad = badlen ? AQ_DEV_BAD_LENGTH : 0;
-    if (lane == 0) {
-        for (int i = 0; i < kStages; ++i) mbar_init(&bars[warp][i], 1);
-        fence_mbar_init();
-    }
-    __syncwarp();
+    const int L = p.seq_lens[b];
+    const bool badlen = L < 0 || L > static_cast<int64_t>(p.max_pages) * P || L > p.max_seq_len;
+    const int np = badlen ? 0 : (L - 1) / P + (L > 0);
+    const int mine = np > w0 ? (np - w0 - 1) / stride + 1 : 0;
     // page k into its ring slot (lane 0); a page outside the pool only arrives
-    auto issue = [&](int k, int pg) {
+    auto issue = [&](int slot, int pg) {
         if (lane == 0) {
-            uint64_t *bar = &bars[warp][k % kStages];
+            uint64_t *bar = &bars[warp][slot];
             if (pg >= 0) {
                 mbar_arrive_expect_tx(bar, kPageBytes);
-                tma_page(stage + (k % kStages) * kPageBytes, &p.map, pg * p.num_kv_heads + kvh, bar);
+                tma_page(stage + slot * kPageBytes, &p.map, pg * p.num_kv_heads + kvh, bar0 + 8 * slot);
             } else {
                 mbar_arrive(bar);
             }
         }
     };
+    float2 sc = page_scales(id);
+    int next_id = mine > 32 ? page_id(32 + lane) : -1;
+    float2 next_sc = make_float2(0.f, 0.f);
 #pragma unroll
     for (int k = 0; k < kStages; ++k) {
         const int pg = __shfl_sync(0xffffffffu, id, k);
         if (k < mine) issue(k, pg);
     }
-    float2 sc = page_scales(id);
-    int next_id = mine > 32 ? page_id(32 + lane) : -1;
 
-    // the query of head r: this lane's 32 dims, scaled by a power of two to
-    // [2^13, 2^14) at its largest magnitude, as fp16 parts
-    uint32_t qh[8][2], ql[8][2];
-    float qs0, qs1;                                    // what undoes it, with the softmax scale: heads 2c, 2c + 1
+    // The queries, once per CTA: a head's 16 threads scale it by a power of two to
+    // [2^13, 2^14) at its largest magnitude and split it into fp16 parts; every warp
+    // then takes its tiles' operand, lane (r, c) head r's dims [32 c, 32 c + 32).
+    // (Groups of 16 words are 20 apart, heads 80: conflict-free both ways.)
     {
-        float4 x[8];
+        const int h = tid / 16, t = tid % 16;
         float top = 0.f;
+        float4 x[2];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            x[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (r < heads) x[j] = *reinterpret_cast<const float4 *>(p.q + (bh0 + r) * D + 32 * c + 4 * j);
+        for (int j = 0; j < 2; ++j) {
+            x[j] = make_float4(__uint_as_float(xq[j].x), __uint_as_float(xq[j].y), __uint_as_float(xq[j].z),
+                               __uint_as_float(xq[j].w));
             top = fmaxf(fmaxf(fmaxf(top, fabsf(x[j].x)), fmaxf(fabsf(x[j].y), fabsf(x[j].z))), fabsf(x[j].w));
         }
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+#pragma unroll
+        for (int off = 1; off < 16; off *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
         const int e = min(253, max(1, 267 - static_cast<int>(__float_as_uint(top) >> 23)));
         const float up = __uint_as_float(static_cast<uint32_t>(e) << 23);
-        const float down = __uint_as_float(static_cast<uint32_t>(254 - e) << 23) * p.scale_log2;
-        qs0 = __shfl_sync(0xffffffffu, down, 8 * c);
-        qs1 = __shfl_sync(0xffffffffu, down, 8 * c + 4);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            f16x2_split(x[j].x * up, x[j].y * up, qh[j][0], ql[j][0]);
-            f16x2_split(x[j].z * up, x[j].w * up, qh[j][1], ql[j][1]);
-        }
+        uint4 hi, lo;
+        f16x2_split(x[0].x * up, x[0].y * up, hi.x, lo.x);
+        f16x2_split(x[0].z * up, x[0].w * up, hi.y, lo.y);
+        f16x2_split(x[1].x * up, x[1].y * up, hi.z, lo.z);
+        f16x2_split(x[1].z * up, x[1].w * up, hi.w, lo.w);
+        const int at = 20 * (t / 4) + 4 * (t % 4);
+        *reinterpret_cast<uint4 *>(&qw[0][h][at]) = hi;
+        *reinterpret_cast<uint4 *>(&qw[1][h][at]) = lo;
+        // what undoes the scaling, with the softmax scale
+        if (t == 0) qdown[h] = __uint_as_float(static_cast<uint32_t>(254 - e) << 23) * p.scale_log2;
     }
-    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f, vref = 0.f;
+    __syncthreads();
+    uint32_t qh[8][2], ql[8][2];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint4 hi = *reinterpret_cast<const uint4 *>(&qw[0][r][20 * c + 4 * j]);
+        const uint4 lo = *reinterpret_cast<const uint4 *>(&qw[1][r][20 * c + 4 * j]);
+        qh[2 * j][0] = hi.x, qh[2 * j][1] = hi.y, qh[2 * j + 1][0] = hi.z, qh[2 * j + 1][1] = hi.w;
+        ql[2 * j][0] = lo.x, ql[2 * j][1] = lo.y, ql[2 * j + 1][0] = lo.z, ql[2 * j + 1][1] = lo.w;
+    }
+    const float qs0 = qdown[2 * c], qs1 = qdown[2 * c + 1];
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f, vref = 0.f, vinv = 1.f;
     float o[8][4];
 #pragma unroll
     for (int j = 0; j < 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-    int bad = 0, k = 0;
+    int bad = badlen ? AQ_DEV_BAD_LENGTH : 0, k = 0, slot = 0;
+    uint32_t phase = 0;
 
 #pragma unroll 1
     for (; k < mine; ++k) {
-        if (k && (k & 31) == 0) {                      // the next 32 pages' ids were fetched 32 pages ago
+        // the next 32 pages: ids fetched 32 pages ahead, scales 16
+        if ((k & 31) == 16) next_sc = page_scales(next_id);
+        if (k && (k & 31) == 0) {
             id = next_id;
-            sc = page_scales(id);
+            sc = next_sc;
             next_id = page_id(k + 32 + lane);
         }
         const int pg = __shfl_sync(0xffffffffu, id, k & 31);
         const float ks = __shfl_sync(0xffffffffu, sc.x, k & 31), vs = __shfl_sync(0xffffffffu, sc.y, k & 31);
-        uint64_t *bar = &bars[warp][k % kStages];
-        const uint32_t phase = (k / kStages) & 1;
+        uint64_t *bar = &bars[warp][slot];
         bool ok = mbar_test_wait(bar, phase);
         if (!ok && p.wait_limit_ns) ok = mbar_wait_limit(bar, phase, p.wait_limit_ns);
         if (!__all_sync(0xffffffffu, ok)) {
             bad |= AQ_DEV_TIMEOUT;
             break;
         }
-        const unsigned char *base = stage + (k % kStages) * kPageBytes;
-        uint4 kr[2][2], v[4];
+        const uint32_t base = stage + slot * kPageBytes;
+        // page k + kStages into this slot, once every lane has read it
+        auto refill = [&]() {
+            __syncwarp();
+            const int n = k + kStages;
+            const int from = __shfl_sync(0xffffffffu, (n ^ k) & 32 ? next_id : id, n & 31);
+            if (n < mine) issue(slot, from);
+            if (++slot == kStages) {
+                slot = 0;
+                phase ^= 1;
+            }
+        };
+        if (pg < 0) {
+            bad |= AQ_DEV_BAD_PAGE;
+            refill();
+            continue;
+        }
+        uint4 kr[2][2];
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                kr[t][i] = *reinterpret_cast<const uint4 *>(base + (8 * t + r) * D + (((2 * c + i) ^ r) << 4));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int t = 2 * c + (i & 1) + 8 * (i >> 1);
-            v[i] = *reinterpret_cast<const uint4 *>(base + (P + t) * D + ((r ^ (t & 7)) << 4));
-        }
-        // every lane has read the slot: refill it
-        __syncwarp();
-        {
-            const int n = k + kStages;
-            const int from = __shfl_sync(0xffffffffu, (n ^ k) & 32 ? next_id : id, n & 31);
-            if (n < mine) issue(n, from);
-        }
-        if (pg < 0) {
-            bad |= AQ_DEV_BAD_PAGE;
-            continue;
-        }
-        const int n = min(P, L - (pg0 + warp + k * kWarps) * P);
+            for (int i = 0; i < 2; ++i) kr[t][i] = lds_v4(base + 8 * t * D + (at_k ^ (16 * i)));
+        const int n = min(P, L - (w0 + k * stride) * P);
 
         float d[2][4] = {};
 #pragma unroll
@@ -268,6 +316,7 @@ __global__ void __launch_bounds__(kThreads, 4) q8_attention_kernel(const __grid_
             m0 = x0;
             m1 = x1;
             vref = vnew;
+            vinv = vref > 0.f ? kWeightTop / vref : 1.f;   // exact: powers of two
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 o[j][0] *= a0 * vr;
@@ -276,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 4) q8_attention_kernel(const __grid_
                 o[j][3] *= a1 * vr;
             }
         }
-        const float vw = vref > 0.f ? kWeightTop * (vs / vref) : vs;
+        const float vw = vs * vinv;
         const float p00 = fast_exp2(s00 - m0), p01 = fast_exp2(s01 - m1), p10 = fast_exp2(s10 - m0), p11 = fast_exp2(s11 - m1);
         l0 += p00 + p10;
         l1 += p01 + p11;
@@ -288,6 +337,11 @@ __global__ void __launch_bounds__(kThreads, 4) q8_attention_kernel(const __grid_
             wh[t] = transpose8(wh[t]);
             wr[t] = transpose8(wr[t]);
         }
+        // values are read (and the slot refilled) this late to stay within 128 registers
+        uint4 v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = lds_v4(base + 8 * (i >> 1) * D + ((i & 1) ? (at_v + D) ^ 16 : at_v));
+        refill();
         if (FMT == kE4m3 && n < P) {                   // slots behind the last token may hold NaN codes
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -306,10 +360,12 @@ __global__ void __launch_bounds__(kThreads, 4) q8_attention_kernel(const __grid_
             }
         }
     }
-    grid_launch_dependents();                          // the combine may be set up
     // a wait that ran out: every copy under way still has to land
     if (bad & AQ_DEV_TIMEOUT)
-        for (int j = k; j < min(mine, k + kStages); ++j) mbar_wait_bounded(&bars[warp][j % kStages], (j / kStages) & 1);
+        for (int j = k; j < min(mine, k + kStages); ++j) {
+            mbar_wait_bounded(&bars[warp][slot], phase);
+            if (++slot == kStages) slot = 0, phase ^= 1;
+        }
 
     // ---- merge the warps (their rings are free now) ------------------------------
 #pragma unroll
@@ -318,17 +374,19 @@ __global__ void __launch_bounds__(kThreads, 4) q8_attention_kernel(const __grid_
         l1 += __shfl_xor_sync(0xffffffffu, l1, off);
     }
     __syncwarp();
-    float(*acc)[D] = reinterpret_cast<float(*)[D]>(stage);
+    // sums in tile order: position 16 j + 2 r + e of a head is dim 16 r + 2 j + e
+    float *acc = reinterpret_cast<float *>(ring + warp * kStages * kPageBytes);
     const float back = vref * (1.f / kWeightTop);
     if (2 * c < heads) {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            *reinterpret_cast<float2 *>(&acc[2 * c][16 * r + 2 * j]) = make_float2(o[j][0] * back, o[j][2] * back);
+            *reinterpret_cast<float2 *>(acc + 2 * c * kSumPitch + 16 * j + 2 * r) = make_float2(o[j][0] * back, o[j][2] * back);
     }
     if (2 * c + 1 < heads) {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            *reinterpret_cast<float2 *>(&acc[2 * c + 1][16 * r + 2 * j]) = make_float2(o[j][1] * back, o[j][3] * back);
+            *reinterpret_cast<float2 *>(acc + (2 * c + 1) * kSumPitch + 16 * j + 2 * r) =
+                make_float2(o[j][1] * back, o[j][3] * back);
     }
     if (r == 0) {
         wm[warp][2 * c] = m0;
@@ -336,76 +394,88 @@ __global__ void __launch_bounds__(kThreads, 4) q8_attention_kernel(const __grid_
         wl[warp][2 * c] = l0;
         wl[warp][2 * c + 1] = l1;
     }
+    if (lane == 0) wbad[warp] = bad;
     __syncthreads();
-    if (bad && lane == 0) atomicOr(&cbad, bad);
-    for (int i = tid; i < heads * D; i += kThreads) {
-        const int g = i / D, dim = i % D;
-        float ms = -INFINITY, num = 0.f, den = 0.f;
+    const int n_out = heads * D, flags = wbad[0] | wbad[1] | wbad[2] | wbad[3];
+    if (flags && tid == 0) flag_status(p.status, flags);
+    const bool merge = p.cluster > 1;
+    auto dim_of = [](int pos) { return (pos & 14) * 8 + (pos >> 4) * 2; };      // of an even position
+    if (tid == 0) cflag = flags;
+    for (int g = warp; g < heads; g += kWarps) {       // a warp per head, 4 positions per lane
+        float f[kWarps], ms = -INFINITY, den = 0.f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) ms = fmaxf(ms, wm[w][g]);
+        float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            if (wm[w][g] > -INFINITY || wl[w][g] != wl[w][g]) {
-                const float f = exp2f(wm[w][g] - ms);
-                den += f * wl[w][g];
-                num += f * reinterpret_cast<const float *>(ring + static_cast<size_t>(w) * kStages * kPageBytes)[i];
+            const float lw = wl[w][g];
+            f[w] = lw != lw ? lw : wm[w][g] > -INFINITY ? fast_exp2(wm[w][g] - ms) : 0.f;
+            const float4 x = *reinterpret_cast<const float4 *>(
+                ring + static_cast<size_t>(w) * kStages * kPageBytes + (g * kSumPitch + 4 * lane) * 4);
+            if (f[w] != 0.f) {                         // (a warp without pages has nothing)
+                den += f[w] * lw;
+                num.x += f[w] * x.x;
+                num.y += f[w] * x.y;
+                num.z += f[w] * x.z;
+                num.w += f[w] * x.w;
             }
         }
-        co[g][dim] = num;
-        if (dim == 0) {
-            cm[g] = ms;
-            cl[g] = den;
-        }
-    }
-    __syncthreads();
-    if (cbad && tid == 0) flag_status(p.status, cbad);
-    if (p.cluster > 1) {
-        // ---- merge the cluster: this CTA's share of the outputs ------------------
-        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-        cluster_wait_acquire();
-        const uint32_t a_o = smem_u32(&co[0][0]), a_m = smem_u32(cm), a_l = smem_u32(cl), a_b = smem_u32(&cbad);
-        for (int i = split * kThreads + tid; i < heads * D; i += S_ * kThreads) {
-            const int g = i / D;
-            float m[kMaxCluster], l[kMaxCluster], x[kMaxCluster], ms = -INFINITY, num = 0.f, den = 0.f;
-            bool flagged = false;
-#pragma unroll
-            for (int s = 0; s < kMaxCluster; ++s) {
-                m[s] = -INFINITY;
-                l[s] = x[s] = 0.f;
-                if (s < S_) {
-                    m[s] = ld_cluster_f32(mapa_u32(a_m + 4 * g, s));
-                    l[s] = ld_cluster_f32(mapa_u32(a_l + 4 * g, s));
-                    x[s] = ld_cluster_f32(mapa_u32(a_o + 4 * i, s));
-                    flagged |= __float_as_int(ld_cluster_f32(mapa_u32(a_b, s))) != 0;
-                }
-                ms = fmaxf(ms, m[s]);
-            }
-#pragma unroll
-            for (int s = 0; s < kMaxCluster; ++s) {
-                if (m[s] > -INFINITY || l[s] != l[s]) {
-                    const float f = exp2f(m[s] - ms);
-                    den += f * l[s];
-                    num += f * x[s];
-                }
-            }
-            p.out[bh0 * D + i] = flagged ? nan : L == 0 ? 0.f : num / den;
-        }
-        asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
-        cluster_wait_acquire();                        // peers have read this CTA's sums
-        return;
-    }
-    for (int i = tid; i < heads * D; i += kThreads) {
-        const int g = i / D, dim = i % D;
-        if (S_ == 1) {
-            p.out[bh0 * D + i] = cbad ? nan : L == 0 ? 0.f : co[g][dim] / cl[g];
+        if (merge) {
+            *reinterpret_cast<float4 *>(co + g * D + 4 * lane) = num;
+            if (lane == 0) cml[g] = make_float2(ms, den);
         } else {
-            p.part_o[((bh0 + g) * S_ + split) * D + dim] = co[g][dim];
-            if (dim == 0) {
-                p.part_ml[((bh0 + g) * S_ + split) * 2] = cbad ? nan : cm[g];
-                p.part_ml[((bh0 + g) * S_ + split) * 2 + 1] = cbad ? nan : cl[g];
+            float *dst = S_ == 1 ? p.out + (bh0 + g) * D : p.part_o + ((bh0 + g) * S_ + split) * D;
+            if (S_ == 1) {
+                const float inv = flags ? nan : L == 0 ? 0.f : 1.f;
+                num.x = inv == 0.f ? 0.f : num.x / den * inv;
+                num.y = inv == 0.f ? 0.f : num.y / den * inv;
+                num.z = inv == 0.f ? 0.f : num.z / den * inv;
+                num.w = inv == 0.f ? 0.f : num.w / den * inv;
+            } else if (lane == 0) {
+                float *ml = p.part_ml + ((bh0 + g) * S_ + split) * 2;
+                ml[0] = flags ? nan : ms;
+                ml[1] = flags ? nan : den;
             }
+            *reinterpret_cast<float2 *>(dst + dim_of(4 * lane)) = make_float2(num.x, num.y);
+            *reinterpret_cast<float2 *>(dst + dim_of(4 * lane + 2)) = make_float2(num.z, num.w);
         }
     }
+    if (!merge) return;
+    __syncwarp();
+    cluster_arrive_release();
+    cluster_wait_acquire();                            // every peer's sums are there
+    // pairs of outputs, shared out over the cluster's threads
+    for (int i = 2 * (split * kThreads + tid); i < n_out; i += 2 * S_ * kThreads) {
+        const int g = i / D;
+        float2 ml[kMaxCluster], x[kMaxCluster];
+        float ms = -INFINITY, den = 0.f;
+        float2 num = make_float2(0.f, 0.f);
+        int flagged = 0;
+#pragma unroll
+        for (int s = 0; s < kMaxCluster; ++s) {
+            ml[s] = make_float2(-INFINITY, 0.f);
+            if (s < S_) {
+                ml[s] = ld_cluster_f32x2(mapa_u32(smem_u32(&cml[g]), s));
+                x[s] = ld_cluster_f32x2(mapa_u32(smem_u32(co + i), s));
+                flagged |= ld_cluster_s32(mapa_u32(smem_u32(&cflag), s));
+            }
+            ms = fmaxf(ms, ml[s].x);
+        }
+#pragma unroll
+        for (int s = 0; s < kMaxCluster; ++s) {
+            if (s < S_ && (ml[s].x > -INFINITY || ml[s].y != ml[s].y)) {
+                const float f = fast_exp2(ml[s].x - ms);
+                den += f * ml[s].y;
+                num.x += f * x[s].x;
+                num.y += f * x[s].y;
+            }
+        }
+        *reinterpret_cast<float2 *>(p.out + (bh0 + g) * D + dim_of(i % D)) =
+            flagged ? make_float2(nan, nan) : L == 0 ? make_float2(0.f, 0.f) : make_float2(num.x / den, num.y / den);
+    }
+    __syncwarp();
+    cluster_arrive_relaxed();
+    cluster_wait_acquire();                            // peers have read this CTA's sums
 }
 
 // out = sum over splits of 2^(m - max) o, over the same sum of l: one CTA per
@@ -413,7 +483,8 @@ __global__ void __launch_bounds__(kThreads, 4) q8_attention_kernel(const __grid_
 // once per CTA, 128 at a time.
 __global__ void __launch_bounds__(kHeadDim) q8_combine_kernel(const __grid_constant__ Q8AttnParams p) {
     __shared__ float wgt[kHeadDim], red[2][kHeadDim / 32];
-    grid_dependency_wait();                            // launched as a dependent of the attention kernel
+    grid_dependency_wait();
+    grid_launch_dependents();
     const size_t bh = static_cast<size_t>(blockIdx.y) * p.num_q_heads + blockIdx.x;
     const int S_ = p.num_splits, d = threadIdx.x;
     const float2 *ml = reinterpret_cast<const float2 *>(p.part_ml) + bh * S_;
@@ -507,20 +578,9 @@ template <int FMT>
 cudaError_t launch_q8(const Q8AttnParams &p, dim3 grid, cudaStream_t s) {
     auto kern = q8_attention_kernel<FMT>;
     static SmemAttr attr_state;
-    if (cudaError_t e = ensure_smem_attr(attr_state, reinterpret_cast<const void *>(kern), kRingBytes); e != cudaSuccess)
+    if (cudaError_t e = ensure_smem_attr(attr_state, reinterpret_cast<const void *>(kern), kRingBytes, 100); e != cudaSuccess)
         return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kRingBytes;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(p.cluster);
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = p.cluster > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kern, p);
+    return launch_dependent(kern, grid, dim3(kThreads), kRingBytes, s, p.cluster, p);
 }
 
 aq_status check_q8(const aq_pq_config *cfg, int32_t batch, int32_t Hq, int32_t Hkv, int32_t max_seq_len,
@@ -603,16 +663,8 @@ aq_status aq_q8_decode_attention(const aq_pq_config *cfg, int32_t format, int32_
                     static_cast<unsigned>(batch));
     e = format == AQ_Q8_INT8 ? launch_q8<kInt8>(p, grid, s) : launch_q8<kE4m3>(p, grid, s);
     if (e == cudaSuccess && pl.workspace > 0) {
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(static_cast<unsigned>(num_q_heads), static_cast<unsigned>(batch));
-        cfg.blockDim = dim3(kHeadDim);
-        cfg.stream = s;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        e = cudaLaunchKernelEx(&cfg, q8_combine_kernel, p);
+        const dim3 rows(static_cast<unsigned>(num_q_heads), static_cast<unsigned>(batch));
+        e = launch_dependent(q8_combine_kernel, rows, dim3(kHeadDim), 0, s, 1, p);
     }
     if (e == cudaSuccess) return AQ_OK;
     record_cuda_error(e);
