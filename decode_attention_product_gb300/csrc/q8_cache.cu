@@ -10,8 +10,8 @@
 // owns the work units from v_b = cu_tokens[b] / 16 + 2 b on: appending n tokens
 // touches at most n / 16 + 2 pages, which v_{b+1} - v_b never undercuts, so the
 // host can size the grid from the token count alone (T / 16 + 2 B + 1 units,
-// two idle ones per request at most) and a warp finds its request by a 32-way
-// search over v.
+// two idle ones per request at most) and a warp finds its request by a search
+// over v: 256 requests in one step, more by 32-way steps.
 #include "common.cuh"
 #include "internal.h"
 #include "q8_common.cuh"
@@ -49,7 +49,7 @@ __device__ __forceinline__ Unit find_unit(const Q8CacheParams &p, int u, int lan
     int b = u, first = u, n = 1, local = 0;
     if (p.cu_tokens) {
         int lo = 0, hi = p.batch;
-        while (hi - lo > 1) {
+        while (hi - lo > 256) {
             const int step = (hi - lo + 31) / 32;
             const int i = lo + lane * step;
             const bool le = i < hi && p.cu_tokens[i] / P + 2 * i <= u;
@@ -58,7 +58,13 @@ __device__ __forceinline__ Unit find_unit(const Q8CacheParams &p, int u, int lan
             lo += k * step;
             hi = min(hi, lo + step);
         }
-        b = lo;
+        int le = 0;                                    // the last 256 at once, 8 per lane
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int i = lo + 8 * lane + j;
+            le += i < hi && p.cu_tokens[i] / P + 2 * i <= u;
+        }
+        b = lo + max(0, static_cast<int>(__reduce_add_sync(0xffffffffu, le)) - 1);
         first = p.cu_tokens[b];
         const int end = p.cu_tokens[b + 1];
         local = u - (first / P + 2 * b);
@@ -96,43 +102,53 @@ __device__ __forceinline__ Unit find_unit(const Q8CacheParams &p, int u, int lan
     return w;
 }
 
-template <int FMT>
-__global__ void __launch_bounds__(kThreads) q8_append_kernel(const __grid_constant__ Q8CacheParams p) {
+// ROWS: the most rows that a block gets from the call (16, or 1 for a decode
+// step's single tokens, which then needs few registers and fills the SMs).
+template <int FMT, int ROWS>
+__global__ void __launch_bounds__(kThreads, ROWS == 1 ? 6 : 2) q8_append_kernel(const __grid_constant__ Q8CacheParams p) {
     constexpr int D = kHeadDim, P = kPage;
+    grid_dependency_wait();
+    grid_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const Unit w = find_unit(p, blockIdx.x, lane, nullptr);
     if (w.page < 0) return;
-    const int pairs = 2 * p.num_kv_heads;
+    const int pairs = 2 * p.num_kv_heads, n = w.s1 - w.s0;
     for (int hp = blockIdx.y * kWarps + warp; hp < pairs; hp += gridDim.y * kWarps) {
         const __half *src = p.kv + (static_cast<size_t>(w.row) * pairs + hp) * D + 4 * lane;
-        uint2 x[P];
+        const size_t block = static_cast<size_t>(w.page) * pairs + hp;
+        uint32_t *dst = reinterpret_cast<uint32_t *>(p.pages + block * (P * D)) + lane;
+        const float old = w.s0 > 0 ? p.scales[block] : 0.f;
+        uint2 x[ROWS];
         uint32_t top = 0;                              // largest |half| bits of each 16-bit lane
 #pragma unroll
-        for (int s = 0; s < P; ++s) {
+        for (int s = 0; s < ROWS; ++s) {
             x[s] = make_uint2(0u, 0u);
-            if (s >= w.s0 && s < w.s1)
-                x[s] = ld_global_na_v2(src + static_cast<size_t>(s - w.s0) * pairs * D);
+            if (s < n) x[s] = ld_global_na_v2(src + static_cast<size_t>(s) * pairs * D);
         }
 #pragma unroll
-        for (int s = 0; s < P; ++s)
+        for (int s = 0; s < ROWS; ++s)
             top = __vmaxu2(top, __vmaxu2(x[s].x & 0x7fff7fffu, x[s].y & 0x7fff7fffu));
         top = max(top & 0xffffu, top >> 16);
         top = __reduce_max_sync(0xffffffffu, top);
-        const size_t block = static_cast<size_t>(w.page) * pairs + hp;
-        const float old = w.s0 > 0 ? p.scales[block] : 0.f;
         // a block that holds a non-finite value is NaN as a whole (codes 0)
         const float want = top >= 0x7c00u ? __int_as_float(0x7fc00000)
                                           : scale_for<FMT>(__half2float(__ushort_as_half(static_cast<unsigned short>(top))));
         const float scale = old != old ? old : (want > old || want != want) ? want : old;
-        uint32_t *dst = reinterpret_cast<uint32_t *>(p.pages + block * (P * D)) + lane;
         if (w.s0 > 0 && scale != old && old == old) {  // earlier tokens of the block, under the grown scale
-            for (int s = 0; s < w.s0; ++s) dst[s * (D / 4)] = rescale4<FMT>(dst[s * (D / 4)], old, scale);
-        }
+            uint32_t c[P];
 #pragma unroll
-        for (int s = 0; s < P; ++s) {
-            if (s >= w.s0 && s < w.s1) {
+            for (int s = 0; s < P - 1; ++s) c[s] = s < w.s0 ? dst[s * (D / 4)] : 0u;
+#pragma unroll
+            for (int s = 0; s < P - 1; ++s)
+                if (s < w.s0) dst[s * (D / 4)] = rescale4<FMT>(c[s], old, scale);
+        }
+        const Encoder enc = encoder_of(scale);
+        dst += w.s0 * (D / 4);
+#pragma unroll
+        for (int s = 0; s < ROWS; ++s) {
+            if (s < n) {
                 const float2 a = h2_to_f2(x[s].x), b = h2_to_f2(x[s].y);
-                dst[s * (D / 4)] = encode4<FMT>(make_float4(a.x, a.y, b.x, b.y), scale);
+                dst[s * (D / 4)] = encode4<FMT>(make_float4(a.x, a.y, b.x, b.y), enc);
             }
         }
         if (lane == 0 && (w.s0 == 0 || scale != old)) p.scales[block] = scale;
@@ -140,24 +156,26 @@ __global__ void __launch_bounds__(kThreads) q8_append_kernel(const __grid_consta
 }
 
 template <int FMT>
-__global__ void __launch_bounds__(kThreads) q8_load_kernel(const __grid_constant__ Q8CacheParams p) {
+__global__ void __launch_bounds__(kThreads, 6) q8_load_kernel(const __grid_constant__ Q8CacheParams p) {
     constexpr int D = kHeadDim, P = kPage;
+    grid_dependency_wait();
+    grid_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     bool bad = false;
     const Unit w = find_unit(p, blockIdx.x, lane, &bad);
     if (w.page < 0 && !bad) return;
-    const int pairs = 2 * p.num_kv_heads;
+    const int pairs = 2 * p.num_kv_heads, n = w.s1 - w.s0;
     for (int hp = blockIdx.y * kWarps + warp; hp < pairs; hp += gridDim.y * kWarps) {
         __half *dst = p.kv + (static_cast<size_t>(w.row) * pairs + hp) * D + 4 * lane;
         const size_t block = static_cast<size_t>(bad ? 0 : w.page) * pairs + hp;
         const float scale = bad ? __int_as_float(0x7fc00000) : p.scales[block];
-        const uint32_t *src = reinterpret_cast<const uint32_t *>(p.pages + block * (P * D)) + lane;
+        const uint32_t *src = reinterpret_cast<const uint32_t *>(p.pages + block * (P * D)) + w.s0 * (D / 4) + lane;
         uint32_t c[P];
 #pragma unroll
-        for (int s = 0; s < P; ++s) c[s] = !bad && s >= w.s0 && s < w.s1 ? src[s * (D / 4)] : 0u;
+        for (int s = 0; s < P; ++s) c[s] = !bad && s < n ? src[s * (D / 4)] : 0u;
 #pragma unroll
         for (int s = 0; s < P; ++s) {
-            if (s >= w.s0 && s < w.s1) {
+            if (s < n) {
                 uint32_t lo, hi;
                 widen4<FMT>(c[s], lo, hi);
                 const float2 a = h2_to_f2(lo), b = h2_to_f2(hi);
@@ -166,7 +184,7 @@ __global__ void __launch_bounds__(kThreads) q8_load_kernel(const __grid_constant
                 uint2 r;
                 r.x = *reinterpret_cast<const uint32_t *>(&l);
                 r.y = *reinterpret_cast<const uint32_t *>(&h);
-                *reinterpret_cast<uint2 *>(dst + static_cast<size_t>(s - w.s0) * pairs * D) = r;
+                *reinterpret_cast<uint2 *>(dst + static_cast<size_t>(s) * pairs * D) = r;
             }
         }
     }
@@ -203,14 +221,11 @@ aq_status q8_cache_call(bool append, const aq_pq_config *cfg, int32_t format, in
                                      : static_cast<unsigned>(batch);
     const dim3 grid(units, static_cast<unsigned>((2 * num_kv_heads + kWarps - 1) / kWarps));
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (append) {
-        if (format == AQ_Q8_INT8) q8_append_kernel<kInt8><<<grid, kThreads, 0, s>>>(p);
-        else q8_append_kernel<kE4m3><<<grid, kThreads, 0, s>>>(p);
-    } else {
-        if (format == AQ_Q8_INT8) q8_load_kernel<kInt8><<<grid, kThreads, 0, s>>>(p);
-        else q8_load_kernel<kE4m3><<<grid, kThreads, 0, s>>>(p);
-    }
-    const cudaError_t e = cudaGetLastError();
+    const bool int8 = format == AQ_Q8_INT8;
+    auto kern = !append      ? (int8 ? q8_load_kernel<kInt8> : q8_load_kernel<kE4m3>)
+                : cu_tokens ? (int8 ? q8_append_kernel<kInt8, kPage> : q8_append_kernel<kE4m3, kPage>)
+                            : (int8 ? q8_append_kernel<kInt8, 1> : q8_append_kernel<kE4m3, 1>);
+    const cudaError_t e = launch_dependent(kern, grid, dim3(kThreads), 0, s, 1, p);
     if (e == cudaSuccess) return AQ_OK;
     record_cuda_error(e);
     return AQ_ERR_CUDA;

@@ -88,19 +88,44 @@ __device__ __forceinline__ float scale_for(float amax) {
     return __uint_as_float(e << 23);
 }
 
-// Four values as codes under `scale` (0 or NaN: codes 0).
+// What turns values into codes under one scale (0 or NaN: codes 0), worked out
+// once per block.
+struct Encoder {
+    float scale, inv;
+    bool exact;                // E4M3: x * inv is x / scale (a power of two, as scale_for gives)
+};
+
+__device__ __forceinline__ Encoder encoder_of(float scale) {
+    Encoder e;
+    e.scale = scale;
+    e.inv = scale > 0.f ? __fdiv_rn(1.0f, scale) : 0.f;
+    e.exact = (__float_as_uint(scale) & 0x7fffffu) == 0u;
+    return e;
+}
+
 template <int FMT>
-__device__ __forceinline__ uint32_t encode4(float4 x, float scale) {
-    if (!(scale > 0.f)) return 0u;
+__device__ __forceinline__ uint32_t encode4(float4 x, const Encoder &e) {
+    if (!(e.scale > 0.f)) return 0u;
     if (FMT == kInt8) {
-        const float inv = __fdiv_rn(1.0f, scale);
-        return (static_cast<uint32_t>(nearest_int8(x.x, scale, inv)) & 0xffu) |
-               ((static_cast<uint32_t>(nearest_int8(x.y, scale, inv)) & 0xffu) << 8) |
-               ((static_cast<uint32_t>(nearest_int8(x.z, scale, inv)) & 0xffu) << 16) |
-               (static_cast<uint32_t>(nearest_int8(x.w, scale, inv)) << 24);
+        // x * inv rounded to an integer by the addition of 1.5 * 2^23 (one rounding), the
+        // code in the low byte.  x * inv is within 127 * 2^-24 of x / scale, so only a
+        // remainder that close to a half needs the exact decision.
+        constexpr float kMagic = 12582912.f;
+        const float f0 = fmaf(x.x, e.inv, kMagic), f1 = fmaf(x.y, e.inv, kMagic);
+        const float f2 = fmaf(x.z, e.inv, kMagic), f3 = fmaf(x.w, e.inv, kMagic);
+        const float r = fmaxf(fmaxf(fabsf(fmaf(x.x, e.inv, kMagic - f0)), fabsf(fmaf(x.y, e.inv, kMagic - f1))),
+                              fmaxf(fabsf(fmaf(x.z, e.inv, kMagic - f2)), fabsf(fmaf(x.w, e.inv, kMagic - f3))));
+        if (r < 0.49998f)
+            return __byte_perm(__byte_perm(__float_as_uint(f0), __float_as_uint(f1), 0x0040),
+                               __byte_perm(__float_as_uint(f2), __float_as_uint(f3), 0x0040), 0x5410);
+        return (static_cast<uint32_t>(nearest_int8(x.x, e.scale, e.inv)) & 0xffu) |
+               ((static_cast<uint32_t>(nearest_int8(x.y, e.scale, e.inv)) & 0xffu) << 8) |
+               ((static_cast<uint32_t>(nearest_int8(x.z, e.scale, e.inv)) & 0xffu) << 16) |
+               (static_cast<uint32_t>(nearest_int8(x.w, e.scale, e.inv)) << 24);
     }
-    return e4m3x2_of(__fdiv_rn(x.x, scale), __fdiv_rn(x.y, scale)) |
-           (e4m3x2_of(__fdiv_rn(x.z, scale), __fdiv_rn(x.w, scale)) << 16);
+    if (e.exact) return e4m3x2_of(x.x * e.inv, x.y * e.inv) | (e4m3x2_of(x.z * e.inv, x.w * e.inv) << 16);
+    return e4m3x2_of(__fdiv_rn(x.x, e.scale), __fdiv_rn(x.y, e.scale)) |
+           (e4m3x2_of(__fdiv_rn(x.z, e.scale), __fdiv_rn(x.w, e.scale)) << 16);
 }
 
 // Four codes of scale `from` rounded again under the larger scale `to`.

@@ -69,6 +69,8 @@ __device__ __forceinline__ float4 turn(float4 x, const float2 (&cs)[4], int lane
 template <bool INTERLEAVED>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeParams p) {
     constexpr int D = kHeadDim;
+    grid_dependency_wait();
+    grid_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t t = blockIdx.x;
     const int pos = max(p.positions[t], -0x7fffffff) - p.lengths;
@@ -196,9 +198,8 @@ aq_status aq_rope(const aq_pq_config *cfg, int32_t num_tokens, int32_t num_q_hea
     if (split > want) split = want;
     const dim3 grid(static_cast<unsigned>(num_tokens), static_cast<unsigned>(split));
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (flags & AQ_ROPE_INTERLEAVED) rope_kernel<true><<<grid, kThreads, 0, s>>>(p);
-    else rope_kernel<false><<<grid, kThreads, 0, s>>>(p);
-    const cudaError_t e = cudaGetLastError();
+    auto kern = flags & AQ_ROPE_INTERLEAVED ? rope_kernel<true> : rope_kernel<false>;
+    const cudaError_t e = launch_dependent(kern, grid, dim3(kThreads), 0, s, 1, p);
     if (e == cudaSuccess) return AQ_OK;
     record_cuda_error(e);
     return AQ_ERR_CUDA;
