@@ -36,16 +36,16 @@ struct Q8CacheParams {
 };
 
 struct Unit {
-    int page;                      // page id, -1: nothing to do
-    int s0, s1;                    // slots [s0, s1) of the page
+    int page;                      // the block table's entry, not checked (kNoPage: no place in the cache)
+    int s0, n;                     // slots [s0, s0 + n) of the page; n == 0: nothing to do
     int64_t row;                   // token row of slot s0
 };
+constexpr int kNoPage = -2147483647 - 1;
 
-// The unit's block range, or page -1; data errors go to the status word and,
-// where `bad` is given, are reported with the rows they concern.
-__device__ __forceinline__ Unit find_unit(const Q8CacheParams &p, int u, int lane, bool *bad) {
+// The unit's rows and block.  A request that does not fit is flagged here.
+__device__ __forceinline__ Unit find_unit(const Q8CacheParams &p, int u, int lane) {
     constexpr int P = kPage;
-    Unit w{-1, 0, 0, 0};
+    Unit w{kNoPage, 0, 0, 0};
     int b = u, first = u, n = 1, local = 0;
     if (p.cu_tokens) {
         int lo = 0, hi = p.batch;
@@ -83,41 +83,38 @@ __device__ __forceinline__ Unit find_unit(const Q8CacheParams &p, int u, int lan
     if (local >= np) return w;
     if (long_) {                                       // no place in the cache: its rows in pieces of 16
         if (lane == 0) flag_status(p.status, AQ_DEV_BAD_LENGTH);
-        w.s1 = min(P, n - local * P);
+        w.n = min(P, n - local * P);
         w.row = first + static_cast<int64_t>(local) * P;
-        if (bad) *bad = true;
         return w;
     }
     const int64_t at = static_cast<int64_t>(p0 + local) * P;
     w.s0 = static_cast<int>(max(start, at) - at);
-    w.s1 = static_cast<int>(min(static_cast<int64_t>(L) - at, static_cast<int64_t>(P)));
+    w.n = static_cast<int>(min(static_cast<int64_t>(L) - at, static_cast<int64_t>(P))) - w.s0;
     w.row = first + (at + w.s0 - start);
-    const int pg = p.block_table[static_cast<size_t>(b) * p.max_pages + p0 + local];
-    if (pg < 0 || pg >= p.num_pages) {
-        if (lane == 0) flag_status(p.status, AQ_DEV_BAD_PAGE);
-        if (bad) *bad = true;
-        return w;
-    }
-    w.page = pg;
+    w.page = p.block_table[static_cast<size_t>(b) * p.max_pages + p0 + local];
     return w;
+}
+
+// Whether the unit's page is one of the pool's; flags one that is not.
+__device__ __forceinline__ bool page_ok(const Q8CacheParams &p, const Unit &w, int lane) {
+    const bool ok = w.page >= 0 && w.page < p.num_pages;
+    if (!ok && w.page != kNoPage && lane == 0) flag_status(p.status, AQ_DEV_BAD_PAGE);
+    return ok;
 }
 
 // ROWS: the most rows that a block gets from the call (16, or 1 for a decode
 // step's single tokens, which then needs few registers and fills the SMs).
 template <int FMT, int ROWS>
-__global__ void __launch_bounds__(kThreads, ROWS == 1 ? 6 : 2) q8_append_kernel(const __grid_constant__ Q8CacheParams p) {
+__global__ void __launch_bounds__(kThreads, ROWS == 1 ? 6 : 4) q8_append_kernel(const __grid_constant__ Q8CacheParams p) {
     constexpr int D = kHeadDim, P = kPage;
     grid_dependency_wait();
     grid_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const Unit w = find_unit(p, blockIdx.x, lane, nullptr);
-    if (w.page < 0) return;
-    const int pairs = 2 * p.num_kv_heads, n = w.s1 - w.s0;
+    const Unit w = find_unit(p, blockIdx.x, lane);
+    const int pairs = 2 * p.num_kv_heads, n = w.n;
+    if (n == 0 || w.page == kNoPage) return;
     for (int hp = blockIdx.y * kWarps + warp; hp < pairs; hp += gridDim.y * kWarps) {
         const __half *src = p.kv + (static_cast<size_t>(w.row) * pairs + hp) * D + 4 * lane;
-        const size_t block = static_cast<size_t>(w.page) * pairs + hp;
-        uint32_t *dst = reinterpret_cast<uint32_t *>(p.pages + block * (P * D)) + lane;
-        const float old = w.s0 > 0 ? p.scales[block] : 0.f;
         uint2 x[ROWS];
         uint32_t top = 0;                              // largest |half| bits of each 16-bit lane
 #pragma unroll
@@ -125,6 +122,10 @@ __global__ void __launch_bounds__(kThreads, ROWS == 1 ? 6 : 2) q8_append_kernel(
             x[s] = make_uint2(0u, 0u);
             if (s < n) x[s] = ld_global_na_v2(src + static_cast<size_t>(s) * pairs * D);
         }
+        if (!page_ok(p, w, lane)) return;              // (the rows were on their way meanwhile)
+        const size_t block = static_cast<size_t>(w.page) * pairs + hp;
+        uint32_t *dst = reinterpret_cast<uint32_t *>(p.pages + block * (P * D)) + lane;
+        const float old = w.s0 > 0 ? p.scales[block] : 0.f;
 #pragma unroll
         for (int s = 0; s < ROWS; ++s)
             top = __vmaxu2(top, __vmaxu2(x[s].x & 0x7fff7fffu, x[s].y & 0x7fff7fffu));
@@ -161,10 +162,10 @@ __global__ void __launch_bounds__(kThreads, 6) q8_load_kernel(const __grid_const
     grid_dependency_wait();
     grid_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    bool bad = false;
-    const Unit w = find_unit(p, blockIdx.x, lane, &bad);
-    if (w.page < 0 && !bad) return;
-    const int pairs = 2 * p.num_kv_heads, n = w.s1 - w.s0;
+    const Unit w = find_unit(p, blockIdx.x, lane);
+    const int pairs = 2 * p.num_kv_heads, n = w.n;
+    if (n == 0) return;
+    const bool bad = !page_ok(p, w, lane);
     for (int hp = blockIdx.y * kWarps + warp; hp < pairs; hp += gridDim.y * kWarps) {
         __half *dst = p.kv + (static_cast<size_t>(w.row) * pairs + hp) * D + 4 * lane;
         const size_t block = static_cast<size_t>(bad ? 0 : w.page) * pairs + hp;
@@ -219,7 +220,11 @@ aq_status q8_cache_call(bool append, const aq_pq_config *cfg, int32_t format, in
     p.max_pages = max_pages;
     const unsigned units = cu_tokens ? static_cast<unsigned>(num_tokens / kPage) + 2u * batch + 1u
                                      : static_cast<unsigned>(batch);
-    const dim3 grid(units, static_cast<unsigned>((2 * num_kv_heads + kWarps - 1) / kWarps));
+    // a unit's heads over several CTAs only as far as that fills the GPU (6 CTAs per SM,
+    // twice): a CTA's first loads depend on one another, its heads' do not
+    unsigned split = static_cast<unsigned>((2 * num_kv_heads + kWarps - 1) / kWarps);
+    if (split > 2u * 6u * 152u / units + 1u) split = 2u * 6u * 152u / units + 1u;
+    const dim3 grid(units, split);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const bool int8 = format == AQ_Q8_INT8;
     auto kern = !append      ? (int8 ? q8_load_kernel<kInt8> : q8_load_kernel<kE4m3>)

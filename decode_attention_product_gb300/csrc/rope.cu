@@ -26,6 +26,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kRows = 4;               // rows of a warp under way together
 
 struct RopeParams {
     const int32_t *positions;      // [T]
@@ -95,28 +96,55 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
         }
     }
     const int w0 = blockIdx.y * kWarps + warp, nw = gridDim.y * kWarps;
+    // kRows rows of a warp at a time: their loads are under way together
     if (p.q && !(pad && q_same)) {
-        for (int h = w0; h < p.num_q_heads; h += nw) {
-            const size_t o = (static_cast<size_t>(t) * p.num_q_heads + h) * D + 4 * lane;
-            const float4 x = *reinterpret_cast<const float4 *>(p.q + o);
-            const float4 y = turn<INTERLEAVED>(x, cs, lane, quarter);
-            if (rot || !q_same) *reinterpret_cast<float4 *>(p.q_out + o) = rot ? y : x;
+        const size_t o = static_cast<size_t>(t) * p.num_q_heads * D + 4 * lane;
+        for (int h0 = w0; h0 < p.num_q_heads; h0 += kRows * nw) {
+            float4 x[kRows];
+#pragma unroll
+            for (int j = 0; j < kRows; ++j) {
+                const int h = h0 + j * nw;
+                x[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (h < p.num_q_heads) x[j] = *reinterpret_cast<const float4 *>(p.q + o + static_cast<size_t>(h) * D);
+            }
+#pragma unroll
+            for (int j = 0; j < kRows; ++j) {
+                const int h = h0 + j * nw;
+                const float4 y = turn<INTERLEAVED>(x[j], cs, lane, quarter);
+                if (h < p.num_q_heads && (rot || !q_same))
+                    *reinterpret_cast<float4 *>(p.q_out + o + static_cast<size_t>(h) * D) = rot ? y : x[j];
+            }
         }
     }
     if (p.kv && !(pad && kv_same)) {
-        for (int h = w0; h < p.num_kv_heads; h += nw) {
-            const size_t o = (static_cast<size_t>(t) * p.num_kv_heads + h) * 2 * D + 4 * lane;
-            const uint2 u = *reinterpret_cast<const uint2 *>(p.kv + o);
-            uint2 v = make_uint2(0u, 0u);
-            if (!kv_same) v = *reinterpret_cast<const uint2 *>(p.kv + o + D);
-            const float2 a = h2_to_f2(u.x), b = h2_to_f2(u.y);
-            const float4 y = turn<INTERLEAVED>(make_float4(a.x, a.y, b.x, b.y), cs, lane, quarter);
-            const __half2 lo = __floats2half2_rn(y.x, y.y), hi = __floats2half2_rn(y.z, y.w);
-            uint2 r;
-            r.x = *reinterpret_cast<const uint32_t *>(&lo);
-            r.y = *reinterpret_cast<const uint32_t *>(&hi);
-            if (rot || !kv_same) *reinterpret_cast<uint2 *>(p.kv_out + o) = rot ? r : u;
-            if (!kv_same) *reinterpret_cast<uint2 *>(p.kv_out + o + D) = v;
+        const size_t o = static_cast<size_t>(t) * p.num_kv_heads * 2 * D + 4 * lane;
+        for (int h0 = w0; h0 < p.num_kv_heads; h0 += kRows * nw) {
+            uint2 u[kRows], v[kRows];
+#pragma unroll
+            for (int j = 0; j < kRows; ++j) {
+                const int h = h0 + j * nw;
+                u[j] = v[j] = make_uint2(0u, 0u);
+                if (h < p.num_kv_heads) {
+                    const __half *row = p.kv + o + static_cast<size_t>(h) * 2 * D;
+                    u[j] = *reinterpret_cast<const uint2 *>(row);
+                    if (!kv_same) v[j] = *reinterpret_cast<const uint2 *>(row + D);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < kRows; ++j) {
+                const int h = h0 + j * nw;
+                const float2 a = h2_to_f2(u[j].x), b = h2_to_f2(u[j].y);
+                const float4 y = turn<INTERLEAVED>(make_float4(a.x, a.y, b.x, b.y), cs, lane, quarter);
+                const __half2 lo = __floats2half2_rn(y.x, y.y), hi = __floats2half2_rn(y.z, y.w);
+                uint2 r;
+                r.x = *reinterpret_cast<const uint32_t *>(&lo);
+                r.y = *reinterpret_cast<const uint32_t *>(&hi);
+                if (h < p.num_kv_heads) {
+                    __half *row = p.kv_out + o + static_cast<size_t>(h) * 2 * D;
+                    if (rot || !kv_same) *reinterpret_cast<uint2 *>(row) = rot ? r : u[j];
+                    if (!kv_same) *reinterpret_cast<uint2 *>(row + D) = v[j];
+                }
+            }
         }
     }
 }
