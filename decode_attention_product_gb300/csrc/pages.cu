@@ -10,8 +10,9 @@
 //
 // "The k-th free page" is a prefix count over refcount.  One launch counts
 // tiles of 4096 pages (and, in its first CTA, prefix-sums what each row needs);
-// the next gives every tile its rank base from the tile counts and hands its
-// free pages out; the last copies page data and publishes lengths.
+// the next gives every tile its rank base from the tile counts and lists the
+// free pages by rank; the last takes each row's pages from that list, copies page
+// data and publishes lengths.  Each launch overlaps the end of the one before.
 #include "common.cuh"
 #include "internal.h"
 
@@ -36,13 +37,18 @@ struct PageParams {
     long long *off;                // [R + 1] prefix of the rows' needs
     int32_t *info;                 // [R]
     int32_t *claim;                // [R]
-    int32_t *pair;                 // [R][2] page to copy from, to
-    int32_t *rank, *movers, *holes;    // [NP]
-    int32_t n, num_rows, max_pages, num_pages, ntiles, num_pools;
+    int32_t *from;                 // [R] shared partial page to copy, or -1
+    int32_t *rank, *movers, *holes;    // [NP]; movers: an extend's free pages by rank
+    int32_t n, num_rows, max_pages, num_pages, ntiles;
 };
 
+// The pools, cut into chunks of kChunk bytes: those of pool k are first[k] ..
+// first[k + 1] - 1.  A warp copies one chunk of one page at a time.
+constexpr int kChunk = 4096;
 struct PagePools {
     aq_page_pool pool[kMaxPools];
+    int32_t first[kMaxPools + 1];
+    int32_t n;
 };
 
 // Exclusive prefix of `v` over the block; *sum = the block's total.
@@ -108,7 +114,7 @@ __device__ __forceinline__ int4 tile_counts(const PageParams &p, int t) {
 // copied first, -1: a data error, the row stays as it is.
 __device__ __forceinline__ int extend_need(const PageParams &p, int i) {
     p.info[i] = -1;
-    p.pair[2 * i] = -1;
+    p.from[i] = -1;
     const int row = p.rows[i], len = p.args[i];
     if (!row_ok(p, row) || __ldcg(&p.claim[row]) != i) {
         flag_status(p.status, AQ_DEV_BAD_ROW);
@@ -128,14 +134,21 @@ __device__ __forceinline__ int extend_need(const PageParams &p, int i) {
             return 0;
         }
         copy = p.refcount[pg] > 1;
+        if (copy) p.from[i] = pg;
     }
     p.info[i] = copy;
     return len > L ? want - have + copy : 0;
 }
 
+__device__ __forceinline__ void begin() {
+    grid_dependency_wait();
+    grid_launch_dependents();
+}
+
 // First launch.  CTA 0 (extend): needs and their prefix.  The others: one tile.
 template <bool EXTEND>
 __global__ void __launch_bounds__(kThreads) pages_count_kernel(const __grid_constant__ PageParams p) {
+    begin();
     if (EXTEND && blockIdx.x == 0) {
         claim_rows(p, p.rows);
         long long base = 0;
@@ -158,90 +171,102 @@ __global__ void __launch_bounds__(kThreads) pages_count_kernel(const __grid_cons
     if (threadIdx.x == 0) p.tiles[t] = sum;
 }
 
-// Sum of the tile counts before tile `t`, and of all of them.
+// Sum of the tile counts before tile `t`, and of all of them (one scan of both).
 __device__ __forceinline__ int tiles_before(const PageParams &p, int t, int *total) {
-    int below = 0, all = 0;
+    unsigned long long both = 0, sum;
     for (int i = threadIdx.x; i < p.ntiles; i += kThreads) {
-        const int x = p.tiles[i];
-        all += x;
-        if (i < t) below += x;
+        const unsigned long long x = static_cast<unsigned>(p.tiles[i]);
+        both += (x << 32) + (i < t ? x : 0u);
     }
-    int sum_below;
-    block_scan(below, &sum_below);
-    block_scan(all, total);
-    return sum_below;
+    block_scan(both, &sum);
+    *total = static_cast<int>(sum >> 32);
+    return static_cast<int>(sum & 0xffffffffu);
 }
 
-// Second launch of an extend: the tile's free pages go to the rows by rank.
+// Second launch of an extend: the lowest free pages, by rank, as many as are needed.
 __global__ void __launch_bounds__(kThreads) pages_assign_kernel(const __grid_constant__ PageParams p) {
+    begin();
+    const int4 r = tile_counts(p, blockIdx.x);
+    const long long need = p.off[p.n];
     int total;
     const int base = tiles_before(p, blockIdx.x, &total);
     if (blockIdx.x == 0 && threadIdx.x == 0) p.total[0] = total;
-    const int4 r = tile_counts(p, blockIdx.x);
     const int f[4] = {r.x == 0, r.y == 0, r.z == 0, r.w == 0};
     int sum;
     int rank = base + block_scan(f[0] + f[1] + f[2] + f[3], &sum);
-    const long long need = p.off[p.n];
-    for (int k = 0; k < 4; ++k) {
-        if (!f[k]) continue;
-        const int mine = rank++;
-        if (mine >= need) return;
-        int lo = 0, hi = p.n;                          // the last entry with off <= mine
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) / 2;
-            if (p.off[mid] <= mine) lo = mid;
-            else hi = mid;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        if (f[k]) {
+            if (rank < need) p.movers[rank] = blockIdx.x * kTile + 4 * threadIdx.x + k;
+            ++rank;
         }
-        if (p.off[lo + 1] > total) continue;           // this row cannot be served: its pages stay free
-        const int pg = blockIdx.x * kTile + 4 * threadIdx.x + k;
-        const int row = p.rows[lo], copy = p.info[lo], j = static_cast<int>(mine - p.off[lo]);
-        int32_t *bt = p.block_table + static_cast<size_t>(row) * p.max_pages + (p.seq_lens[row] + kPage - 1) / kPage - copy + j;
-        if (copy && j == 0) {
-            p.pair[2 * lo] = *bt;
-            p.pair[2 * lo + 1] = pg;
-        }
-        *bt = pg;
-        p.refcount[pg] = 1;
+}
+
+// Chunk c of page `from` to page `to`, by one warp: up to 8 loads of 16 bytes per
+// lane under way.  Pages that are no multiple of 16 bytes move by words.
+__device__ __forceinline__ void copy_chunk(const PagePools &pools, int64_t from, int64_t to, int c, int lane) {
+    int lo = 0, hi = pools.n;                          // the pool of chunk c
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (pools.first[mid] <= c) lo = mid;
+        else hi = mid;
+    }
+    const int64_t bytes = pools.pool[lo].page_bytes, at = static_cast<int64_t>(c - pools.first[lo]) * kChunk;
+    const int n = static_cast<int>(min(bytes - at, static_cast<int64_t>(kChunk)));
+    unsigned char *data = static_cast<unsigned char *>(pools.pool[lo].data);
+    const unsigned char *src = data + from * bytes + at;
+    unsigned char *dst = data + to * bytes + at;
+    if (bytes % 16 == 0) {
+        uint4 x[kChunk / 512];
+#pragma unroll
+        for (int j = 0; j < kChunk / 512; ++j)
+            if (512 * j + 16 * lane < n) x[j] = ld_global_na_v4(src + 512 * j + 16 * lane);
+#pragma unroll
+        for (int j = 0; j < kChunk / 512; ++j)
+            if (512 * j + 16 * lane < n) *reinterpret_cast<uint4 *>(dst + 512 * j + 16 * lane) = x[j];
+    } else {
+        for (int i = 4 * lane; i < n; i += 128)
+            *reinterpret_cast<uint32_t *>(dst + i) = *reinterpret_cast<const uint32_t *>(src + i);
     }
 }
 
-// One page of every pool, this CTA's part of `parts`.
-__device__ __forceinline__ void copy_page(const PagePools &pools, int num_pools, int from, int to, int part, int parts) {
-    const int step = parts * blockDim.x, first = part * blockDim.x + threadIdx.x;
-    for (int k = 0; k < num_pools; ++k) {
-        const int64_t bytes = pools.pool[k].page_bytes;
-        unsigned char *data = static_cast<unsigned char *>(pools.pool[k].data);
-        if (bytes % 16 == 0) {
-            const uint4 *s = reinterpret_cast<const uint4 *>(data + from * bytes);
-            uint4 *d = reinterpret_cast<uint4 *>(data + to * bytes);
-            for (int64_t i = first; i < bytes / 16; i += step) d[i] = s[i];
-        } else {
-            const uint32_t *s = reinterpret_cast<const uint32_t *>(data + from * bytes);
-            uint32_t *d = reinterpret_cast<uint32_t *>(data + to * bytes);
-            for (int64_t i = first; i < bytes / 4; i += step) d[i] = s[i];
-        }
-    }
-}
-
-// Last launch of an extend: shared partial pages are copied, the copies' old
-// references dropped and the new lengths published.
+// Last launch of an extend, CTAs (row entry, part): the row's new table entries,
+// its reference to a shared partial page dropped and the page copied, its length
+// published.
 __global__ void __launch_bounds__(kCopyThreads) pages_grow_kernel(const __grid_constant__ PageParams p,
                                                                   const __grid_constant__ PagePools pools) {
-    const int i = blockIdx.x;
-    if (p.info[i] < 0) return;
-    const bool served = p.off[i + 1] <= p.total[0];
-    if (blockIdx.y == 0 && threadIdx.x == 0) {
-        if (served) p.seq_lens[p.rows[i]] = p.args[i];
-        else flag_status(p.status, AQ_DEV_NO_PAGE);
+    begin();
+    const int i = blockIdx.x, copy = p.info[i];
+    if (copy < 0) return;
+    const long long at = p.off[i], end = p.off[i + 1];
+    if (end > p.total[0] && end > at) {                // (a row that needs no page is served in any case)
+        if (blockIdx.y == 0 && threadIdx.x == 0) flag_status(p.status, AQ_DEV_NO_PAGE);
+        return;
     }
-    const int from = p.pair[2 * i];
-    if (!served || from < 0) return;
-    if (blockIdx.y == 0 && threadIdx.x == 0) atomicSub(&p.refcount[from], 1);
-    copy_page(pools, p.num_pools, from, p.pair[2 * i + 1], blockIdx.y, gridDim.y);
+    const int from = p.from[i];
+    if (blockIdx.y == 0) {
+        const int row = p.rows[i], len = p.args[i], want = (len + kPage - 1) / kPage;
+        const int first = want - static_cast<int>(end - at);               // the copied page's entry among them
+        int32_t *bt = p.block_table + static_cast<size_t>(row) * p.max_pages;
+        for (int j = threadIdx.x; j < want - first; j += kCopyThreads) {
+            const int pg = p.movers[at + j];
+            bt[first + j] = pg;
+            p.refcount[pg] = 1;
+        }
+        if (threadIdx.x == 0) {
+            p.seq_lens[row] = len;
+            if (copy) atomicSub(&p.refcount[from], 1);
+        }
+    }
+    if (!copy) return;
+    const int to = p.movers[at], chunks = pools.first[pools.n];
+    for (int c = blockIdx.y * (kCopyThreads / 32) + threadIdx.x / 32; c < chunks; c += gridDim.y * (kCopyThreads / 32))
+        copy_chunk(pools, from, to, c, threadIdx.x & 31);
 }
 
 // Fork: which entries hold (the destination is an empty row, named once).
 __global__ void __launch_bounds__(kThreads) pages_fork_check_kernel(const __grid_constant__ PageParams p) {
+    begin();
     claim_rows(p, p.args);
     for (int i = threadIdx.x; i < p.n; i += kThreads) {
         const int src = p.rows[i], dst = p.args[i];
@@ -255,6 +280,7 @@ __global__ void __launch_bounds__(kThreads) pages_fork_check_kernel(const __grid
 }
 
 __global__ void __launch_bounds__(kCopyThreads) pages_fork_kernel(const __grid_constant__ PageParams p) {
+    begin();
     const int i = blockIdx.x, L = p.info[i];
     if (L < 0) return;
     const int32_t *src = p.block_table + static_cast<size_t>(p.rows[i]) * p.max_pages;
@@ -272,6 +298,7 @@ __global__ void __launch_bounds__(kCopyThreads) pages_fork_kernel(const __grid_c
 // named twice lose each page once, whichever entry comes first.
 __global__ void __launch_bounds__(kCopyThreads) pages_free_kernel(const __grid_constant__ PageParams p) {
     __shared__ int len;
+    begin();
     const int row = p.rows[blockIdx.x], keep = p.args ? p.args[blockIdx.x] : 0;
     if (threadIdx.x == 0) {
         len = 0;
@@ -298,28 +325,26 @@ __global__ void __launch_bounds__(kCopyThreads) pages_free_kernel(const __grid_c
 // mover of rank (live pages in [N, p)), free page p < N the hole of rank (free
 // pages in [0, p)); there are as many movers as holes.
 __global__ void __launch_bounds__(kThreads) pages_map_kernel(const __grid_constant__ PageParams p) {
+    begin();
+    const int4 r = tile_counts(p, blockIdx.x);
     int live;
     const int base = tiles_before(p, blockIdx.x, &live);
     // live pages below N: whole tiles, and the part of the tile that holds N
-    int below;
     const int cut = live / kTile;
     int under = 0;
-    {
-        int dummy;
-        under = tiles_before(p, cut, &dummy);
-        if (cut < p.ntiles) {
-            const int4 r = tile_counts(p, cut);
-            const int i = cut * kTile + 4 * threadIdx.x;
-            const int n = (r.x > 0 && i < live) + (r.y > 0 && i + 1 < live) + (r.z > 0 && i + 2 < live) + (r.w > 0 && i + 3 < live);
-            block_scan(n, &below);
-            under += below;
-        }
+    if (cut < p.ntiles) {
+        const int4 s = tile_counts(p, cut);
+        const int i = cut * kTile + 4 * threadIdx.x;
+        int n = (s.x > 0 && i < live) + (s.y > 0 && i + 1 < live) + (s.z > 0 && i + 2 < live) + (s.w > 0 && i + 3 < live);
+        for (int t = threadIdx.x; t < cut; t += kThreads) n += p.tiles[t];
+        block_scan(n, &under);
+    } else {
+        under = live;                                  // every page is live
     }
     if (blockIdx.x == 0 && threadIdx.x == 0) {
         p.total[0] = live;
         p.total[1] = live - under;
     }
-    const int4 r = tile_counts(p, blockIdx.x);
     const int c[4] = {r.x, r.y, r.z, r.w};
     int sum;
     int before = base + block_scan((c[0] > 0) + (c[1] > 0) + (c[2] > 0) + (c[3] > 0), &sum);
@@ -344,7 +369,8 @@ __global__ void __launch_bounds__(kThreads) pages_map_kernel(const __grid_consta
 // table rewritten (the first `table_ctas` CTAs).
 __global__ void __launch_bounds__(kCopyThreads) pages_move_kernel(const __grid_constant__ PageParams p,
                                                                   const __grid_constant__ PagePools pools,
-                                                                  int table_ctas, int parts) {
+                                                                  int table_ctas) {
+    begin();
     const int live = p.total[0], moves = p.total[1];
     if (static_cast<int>(blockIdx.x) < table_ctas) {
         for (int row = blockIdx.x; row < p.num_rows; row += table_ctas) {
@@ -364,15 +390,17 @@ __global__ void __launch_bounds__(kCopyThreads) pages_move_kernel(const __grid_c
         }
         return;
     }
-    const int64_t units = static_cast<int64_t>(moves) * parts;
-    for (int64_t u = blockIdx.x - table_ctas; u < units; u += gridDim.x - table_ctas) {
-        const int64_t i = u / parts;
-        const int from = p.movers[i], to = p.holes[i];
-        if (u % parts == 0 && threadIdx.x == 0) {
-            p.refcount[to] = p.refcount[from];
-            p.refcount[from] = 0;
-        }
-        copy_page(pools, p.num_pools, from, to, static_cast<int>(u % parts), parts);
+    const int chunks = pools.first[pools.n], lane = threadIdx.x & 31;
+    const int64_t w0 = static_cast<int64_t>(blockIdx.x - table_ctas) * (kCopyThreads / 32) + threadIdx.x / 32;
+    const int64_t nw = static_cast<int64_t>(gridDim.x - table_ctas) * (kCopyThreads / 32);
+    for (int64_t i = w0 * 32 + lane; i < moves; i += nw * 32) {
+        const int from = p.movers[i];
+        p.refcount[p.holes[i]] = p.refcount[from];
+        p.refcount[from] = 0;
+    }
+    for (int64_t u = w0; u < static_cast<int64_t>(moves) * chunks; u += nw) {
+        const int64_t i = u / chunks;
+        copy_chunk(pools, p.movers[i], p.holes[i], static_cast<int>(u % chunks), lane);
     }
 }
 
@@ -384,7 +412,7 @@ int tiles_of(int64_t pages) { return static_cast<int>((pages + kTile - 1) / kTil
 size_t ints(int64_t n) { return static_cast<size_t>((n + 3) / 4 * 4); }
 
 size_t workspace_ints(int32_t rows, int64_t pages) {
-    return ints(tiles_of(pages)) + 4 + ints(2 * (int64_t(rows) + 1)) + 2 * ints(rows) + ints(2 * int64_t(rows)) + 3 * ints(pages);
+    return ints(tiles_of(pages)) + 4 + ints(2 * (int64_t(rows) + 1)) + 3 * ints(rows) + 3 * ints(pages);
 }
 
 aq_status check_pages(int32_t n, int32_t num_rows, int32_t max_pages, int64_t num_pages) {
@@ -400,6 +428,8 @@ aq_status check_pools(const aq_page_pool *pools, int32_t num_pools) {
     for (int k = 0; k < num_pools; ++k)
         if (!pools[k].data || off16(pools[k].data) || pools[k].page_bytes < 4 || pools[k].page_bytes % 4)
             return AQ_ERR_INVALID_ARGUMENT;
+    for (int k = 0; k < num_pools; ++k)                // (chunks are counted in 32 bits)
+        if (pools[k].page_bytes > (1ll << 34)) return AQ_ERR_UNSUPPORTED;
     return AQ_OK;
 }
 
@@ -425,24 +455,25 @@ PageParams page_params(int32_t n, const int32_t *rows, const int32_t *args, int3
         p.off = reinterpret_cast<long long *>(p.total + 4);
         p.info = p.total + 4 + ints(2 * (int64_t(num_rows) + 1));
         p.claim = p.info + ints(num_rows);
-        p.pair = p.claim + ints(num_rows);
-        p.rank = p.pair + ints(2 * int64_t(num_rows));
+        p.from = p.claim + ints(num_rows);
+        p.rank = p.from + ints(num_rows);
         p.movers = p.rank + ints(num_pages);
         p.holes = p.movers + ints(num_pages);
     }
     return p;
 }
 
-// CTAs per page copy: 16 KiB each, 64 at most.
-int copy_parts(const PagePools &pools, int num_pools) {
-    int64_t bytes = 0;
-    for (int k = 0; k < num_pools; ++k) bytes = pools.pool[k].page_bytes > bytes ? pools.pool[k].page_bytes : bytes;
-    const int64_t parts = (bytes + 16383) / 16384;
-    return static_cast<int>(parts < 1 ? 1 : parts > 64 ? 64 : parts);
+PagePools page_pools(const aq_page_pool *pools, int32_t num_pools) {
+    PagePools pl{};
+    pl.n = num_pools;
+    for (int k = 0; k < num_pools; ++k) {
+        pl.pool[k] = pools[k];
+        pl.first[k + 1] = pl.first[k] + static_cast<int32_t>((pools[k].page_bytes + kChunk - 1) / kChunk);
+    }
+    return pl;
 }
 
-aq_status done() {
-    const cudaError_t e = cudaGetLastError();
+aq_status done(cudaError_t e) {
     if (e == cudaSuccess) return AQ_OK;
     record_cuda_error(e);
     return AQ_ERR_CUDA;
@@ -477,16 +508,19 @@ aq_status aq_pages_extend(int32_t n, const int32_t *rows, const int32_t *new_len
     if (!workspace || workspace_bytes < workspace_ints(num_rows, num_pages) * sizeof(int32_t))
         return AQ_ERR_WORKSPACE_TOO_SMALL;
     if (off16(workspace)) return AQ_ERR_INVALID_ARGUMENT;
-    PageParams p = page_params(n, rows, new_lens, block_table, num_rows, max_pages, seq_lens, refcount, num_pages,
-                               workspace, device_status);
-    p.num_pools = num_pools;
-    PagePools pl{};
-    for (int k = 0; k < num_pools; ++k) pl.pool[k] = pools[k];
+    const PageParams p = page_params(n, rows, new_lens, block_table, num_rows, max_pages, seq_lens, refcount, num_pages,
+                                     workspace, device_status);
+    const PagePools pl = page_pools(pools, num_pools);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    pages_count_kernel<true><<<p.ntiles + 1, kThreads, 0, s>>>(p);
-    pages_assign_kernel<<<p.ntiles > 0 ? p.ntiles : 1, kThreads, 0, s>>>(p);
-    pages_grow_kernel<<<dim3(n, copy_parts(pl, num_pools)), kCopyThreads, 0, s>>>(p, pl);
-    return done();
+    // a page's chunks over at most 64 CTAs of 8 warps
+    const int parts = (pl.first[num_pools] + 7) / 8;
+    cudaError_t e = launch_dependent(pages_count_kernel<true>, dim3(p.ntiles + 1), dim3(kThreads), 0, s, 1, p);
+    if (e == cudaSuccess)
+        e = launch_dependent(pages_assign_kernel, dim3(p.ntiles > 0 ? p.ntiles : 1), dim3(kThreads), 0, s, 1, p);
+    if (e == cudaSuccess)
+        e = launch_dependent(pages_grow_kernel, dim3(n, parts < 1 ? 1 : parts > 64 ? 64 : parts), dim3(kCopyThreads), 0, s,
+                             1, p, pl);
+    return done(e);
 }
 
 aq_status aq_pages_fork(int32_t n, const int32_t *src_rows, const int32_t *dst_rows, int32_t *block_table,
@@ -504,10 +538,12 @@ aq_status aq_pages_fork(int32_t n, const int32_t *src_rows, const int32_t *dst_r
     const PageParams p = page_params(n, src_rows, dst_rows, block_table, num_rows, max_pages, seq_lens, refcount,
                                      num_pages, workspace, device_status);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    pages_fork_check_kernel<<<1, kThreads, 0, s>>>(p);
+    cudaError_t e = launch_dependent(pages_fork_check_kernel, dim3(1), dim3(kThreads), 0, s, 1, p);
     const int parts = (max_pages + 4 * kCopyThreads - 1) / (4 * kCopyThreads);
-    pages_fork_kernel<<<dim3(n, parts < 1 ? 1 : parts > 64 ? 64 : parts), kCopyThreads, 0, s>>>(p);
-    return done();
+    if (e == cudaSuccess)
+        e = launch_dependent(pages_fork_kernel, dim3(n, parts < 1 ? 1 : parts > 64 ? 64 : parts), dim3(kCopyThreads), 0, s,
+                             1, p);
+    return done(e);
 }
 
 aq_status aq_pages_free(int32_t n, const int32_t *rows, const int32_t *keep_lens, int32_t *block_table,
@@ -519,8 +555,8 @@ aq_status aq_pages_free(int32_t n, const int32_t *rows, const int32_t *keep_lens
     if (!rows || !block_table || !seq_lens || (num_pages > 0 && !refcount) || off16(refcount)) return AQ_ERR_INVALID_ARGUMENT;
     const PageParams p = page_params(n, rows, keep_lens, block_table, num_rows, max_pages, seq_lens, refcount,
                                      num_pages, nullptr, device_status);
-    pages_free_kernel<<<n, kCopyThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
-    return done();
+    return done(launch_dependent(pages_free_kernel, dim3(n), dim3(kCopyThreads), 0, reinterpret_cast<cudaStream_t>(stream),
+                                 1, p));
 }
 
 aq_status aq_pages_compact(int32_t *block_table, int32_t num_rows, int32_t max_pages, int32_t *seq_lens,
@@ -534,17 +570,16 @@ aq_status aq_pages_compact(int32_t *block_table, int32_t num_rows, int32_t max_p
     if (!workspace || workspace_bytes < workspace_ints(num_rows, num_pages) * sizeof(int32_t))
         return AQ_ERR_WORKSPACE_TOO_SMALL;
     if (off16(workspace)) return AQ_ERR_INVALID_ARGUMENT;
-    PageParams p = page_params(0, nullptr, nullptr, block_table, num_rows, max_pages, seq_lens, refcount, num_pages,
-                               workspace, device_status);
-    p.num_pools = num_pools;
-    PagePools pl{};
-    for (int k = 0; k < num_pools; ++k) pl.pool[k] = pools[k];
+    const PageParams p = page_params(0, nullptr, nullptr, block_table, num_rows, max_pages, seq_lens, refcount, num_pages,
+                                     workspace, device_status);
+    const PagePools pl = page_pools(pools, num_pools);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    pages_count_kernel<false><<<p.ntiles, kThreads, 0, s>>>(p);
-    pages_map_kernel<<<p.ntiles, kThreads, 0, s>>>(p);
     const int table = num_rows < 152 ? num_rows : 152;
-    pages_move_kernel<<<table + 152 * 6, kCopyThreads, 0, s>>>(p, pl, table, copy_parts(pl, num_pools));
-    return done();
+    cudaError_t e = launch_dependent(pages_count_kernel<false>, dim3(p.ntiles), dim3(kThreads), 0, s, 1, p);
+    if (e == cudaSuccess) e = launch_dependent(pages_map_kernel, dim3(p.ntiles), dim3(kThreads), 0, s, 1, p);
+    if (e == cudaSuccess)
+        e = launch_dependent(pages_move_kernel, dim3(table + 152 * 5), dim3(kCopyThreads), 0, s, 1, p, pl, table);
+    return done(e);
 }
 
 }  // extern "C"

@@ -615,7 +615,8 @@ aq_status aq_q8_decode_attention(const aq_pq_config *cfg, int32_t format, int32_
  *                  tokens' slots are not written.  A row named twice
  *                  (AQ_DEV_BAD_ROW) counts once, by its first entry.  Rows are
  *                  served in order: a row whose pages, with those of the rows
- *                  before it, exceed the free ones sets AQ_DEV_NO_PAGE.
+ *                  before it, exceed the free ones sets AQ_DEV_NO_PAGE (one
+ *                  that needs no page is served).
  * aq_pages_fork    the empty row dst_rows[i] becomes a copy of src_rows[i],
  *                  sharing all its pages.  A destination that is not empty, or
  *                  named before, sets AQ_DEV_BAD_ROW.

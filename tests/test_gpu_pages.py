@@ -63,7 +63,7 @@ class Model:
             used += want - have + copy
         for r, n, have, want, copy, at in plan:
             need = want - have + copy
-            if at + need > len(free):
+            if need and at + need > len(free):
                 self.status |= NO_PAGE
                 continue
             new = free[at:at + need]
