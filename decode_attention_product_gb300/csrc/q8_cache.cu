@@ -136,21 +136,35 @@ __global__ void __launch_bounds__(kThreads, ROWS == 1 ? 6 : 4) q8_append_kernel(
                                           : scale_for<FMT>(__half2float(__ushort_as_half(static_cast<unsigned short>(top))));
         const float scale = old != old ? old : (want > old || want != want) ? want : old;
         if (w.s0 > 0 && scale != old && old == old) {  // earlier tokens of the block, under the grown scale
-            uint32_t c[P];
+            // four rows under way together; rolled, so that its code does not crowd out the rest
+#pragma unroll 1
+            for (int s = 0; s < w.s0; s += 4) {
+                uint32_t c[4];
 #pragma unroll
-            for (int s = 0; s < P - 1; ++s) c[s] = s < w.s0 ? dst[s * (D / 4)] : 0u;
+                for (int j = 0; j < 4; ++j) c[j] = s + j < w.s0 ? dst[(s + j) * (D / 4)] : 0u;
 #pragma unroll
-            for (int s = 0; s < P - 1; ++s)
-                if (s < w.s0) dst[s * (D / 4)] = rescale4<FMT>(c[s], old, scale);
+                for (int j = 0; j < 4; ++j)
+                    if (s + j < w.s0) dst[(s + j) * (D / 4)] = rescale4<FMT>(c[j], old, scale);
+            }
         }
-        const Encoder enc = encoder_of(scale);
+        const Encoder enc = encoder_of<FMT>(scale);
         dst += w.s0 * (D / 4);
+        uint32_t redo = 0;
 #pragma unroll
         for (int s = 0; s < ROWS; ++s) {
             if (s < n) {
                 const float2 a = h2_to_f2(x[s].x), b = h2_to_f2(x[s].y);
-                dst[s * (D / 4)] = encode4<FMT>(make_float4(a.x, a.y, b.x, b.y), enc);
+                bool again;
+                dst[s * (D / 4)] = encode4<FMT>(make_float4(a.x, a.y, b.x, b.y), enc, again);
+                redo |= again ? 1u << s : 0u;
             }
+        }
+        while (redo) {                                 // few rows, if any: fetched again, decided exactly
+            const int s = __ffs(redo) - 1;
+            redo &= redo - 1;
+            const uint2 y = ld_global_na_v2(src + static_cast<size_t>(s) * pairs * D);
+            const float2 a = h2_to_f2(y.x), b = h2_to_f2(y.y);
+            dst[s * (D / 4)] = encode4_exact<FMT>(make_float4(a.x, a.y, b.x, b.y), scale);
         }
         if (lane == 0 && (w.s0 == 0 || scale != old)) p.scales[block] = scale;
     }

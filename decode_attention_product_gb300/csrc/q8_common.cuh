@@ -88,44 +88,58 @@ __device__ __forceinline__ float scale_for(float amax) {
     return __uint_as_float(e << 23);
 }
 
-// What turns values into codes under one scale (0 or NaN: codes 0), worked out
-// once per block.
+// What turns values into codes under one scale, worked out once per block.
+// INT8: x * lo and x * hi, lo and hi a few units of 2^-24 below and above 1 / scale,
+// are rounded to integers by the addition of 1.5 * 2^23 (one rounding, the code in
+// the low byte).  x / scale lies between the two products: where they round alike
+// the code is decided, else (a quotient within 2^-15 of a half) x is looked at
+// exactly.  E4M3: x * lo is x / scale itself (a power of two).
 struct Encoder {
-    float scale, inv;
-    bool exact;                // E4M3: x * inv is x / scale (a power of two, as scale_for gives)
+    float scale, lo, hi;
+    uint32_t keep;             // 0 where every code is 0 (scale 0 or NaN)
+    bool all;                  // every value is looked at exactly (E4M3, a scale scale_for does not give)
 };
 
+template <int FMT>
 __device__ __forceinline__ Encoder encoder_of(float scale) {
     Encoder e;
+    const float inv = scale > 0.f ? __fdiv_rn(1.0f, scale) : 0.f;
     e.scale = scale;
-    e.inv = scale > 0.f ? __fdiv_rn(1.0f, scale) : 0.f;
-    e.exact = (__float_as_uint(scale) & 0x7fffffu) == 0u;
+    e.lo = FMT == kInt8 ? inv * (1.f - 0x1p-22f) : inv;
+    e.hi = inv * (1.f + 0x1p-22f);
+    e.keep = scale > 0.f ? 0xffffffffu : 0u;
+    e.all = FMT == kE4m3 && scale > 0.f && (__float_as_uint(scale) & 0x7fffffu) != 0u;
     return e;
 }
 
+// Four values as codes; `again` where the exact decision has to be taken.
 template <int FMT>
-__device__ __forceinline__ uint32_t encode4(float4 x, const Encoder &e) {
-    if (!(e.scale > 0.f)) return 0u;
+__device__ __forceinline__ uint32_t encode4(float4 x, const Encoder &e, bool &again) {
     if (FMT == kInt8) {
-        // x * inv rounded to an integer by the addition of 1.5 * 2^23 (one rounding), the
-        // code in the low byte.  x * inv is within 127 * 2^-24 of x / scale, so only a
-        // remainder that close to a half needs the exact decision.
-        constexpr float kMagic = 12582912.f;
-        const float f0 = fmaf(x.x, e.inv, kMagic), f1 = fmaf(x.y, e.inv, kMagic);
-        const float f2 = fmaf(x.z, e.inv, kMagic), f3 = fmaf(x.w, e.inv, kMagic);
-        const float r = fmaxf(fmaxf(fabsf(fmaf(x.x, e.inv, kMagic - f0)), fabsf(fmaf(x.y, e.inv, kMagic - f1))),
-                              fmaxf(fabsf(fmaf(x.z, e.inv, kMagic - f2)), fabsf(fmaf(x.w, e.inv, kMagic - f3))));
-        if (r < 0.49998f)
-            return __byte_perm(__byte_perm(__float_as_uint(f0), __float_as_uint(f1), 0x0040),
-                               __byte_perm(__float_as_uint(f2), __float_as_uint(f3), 0x0040), 0x5410);
-        return (static_cast<uint32_t>(nearest_int8(x.x, e.scale, e.inv)) & 0xffu) |
-               ((static_cast<uint32_t>(nearest_int8(x.y, e.scale, e.inv)) & 0xffu) << 8) |
-               ((static_cast<uint32_t>(nearest_int8(x.z, e.scale, e.inv)) & 0xffu) << 16) |
-               (static_cast<uint32_t>(nearest_int8(x.w, e.scale, e.inv)) << 24);
+        auto round4 = [&](float inv) {
+            constexpr float kMagic = 12582912.f;
+            const uint32_t a = __float_as_uint(fmaf(x.x, inv, kMagic)), b = __float_as_uint(fmaf(x.y, inv, kMagic));
+            const uint32_t c = __float_as_uint(fmaf(x.z, inv, kMagic)), d = __float_as_uint(fmaf(x.w, inv, kMagic));
+            return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410) & e.keep;
+        };
+        const uint32_t w = round4(e.lo);
+        again = w != round4(e.hi);
+        return w;
     }
-    if (e.exact) return e4m3x2_of(x.x * e.inv, x.y * e.inv) | (e4m3x2_of(x.z * e.inv, x.w * e.inv) << 16);
-    return e4m3x2_of(__fdiv_rn(x.x, e.scale), __fdiv_rn(x.y, e.scale)) |
-           (e4m3x2_of(__fdiv_rn(x.z, e.scale), __fdiv_rn(x.w, e.scale)) << 16);
+    again = e.all;
+    return (e4m3x2_of(x.x * e.lo, x.y * e.lo) | (e4m3x2_of(x.z * e.lo, x.w * e.lo) << 16)) & e.keep;
+}
+
+template <int FMT>
+__device__ __forceinline__ uint32_t encode4_exact(float4 x, float scale) {
+    const float inv = __fdiv_rn(1.0f, scale);
+    if (FMT == kInt8)
+        return (static_cast<uint32_t>(nearest_int8(x.x, scale, inv)) & 0xffu) |
+               ((static_cast<uint32_t>(nearest_int8(x.y, scale, inv)) & 0xffu) << 8) |
+               ((static_cast<uint32_t>(nearest_int8(x.z, scale, inv)) & 0xffu) << 16) |
+               (static_cast<uint32_t>(nearest_int8(x.w, scale, inv)) << 24);
+    return e4m3x2_of(__fdiv_rn(x.x, scale), __fdiv_rn(x.y, scale)) |
+           (e4m3x2_of(__fdiv_rn(x.z, scale), __fdiv_rn(x.w, scale)) << 16);
 }
 
 // Four codes of scale `from` rounded again under the larger scale `to`.
