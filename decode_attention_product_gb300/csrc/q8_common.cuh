@@ -78,6 +78,15 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t &lo, uint32_t &hi) {
     }
 }
 
+// Four E4M3 codes as fp16 pairs of their values times 2^-8, by integer operations:
+// sign, exponent and fraction moved to an fp16's places (subnormals stay exact; the
+// codes are finite).
+__device__ __forceinline__ void shift4_e4m3(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    const uint32_t top = ((w >> 1) & 0x3f3f3f3fu) | (w & 0x80808080u), low = (w << 7) & 0x80808080u;
+    lo = __byte_perm(low, top, 0x5140);
+    hi = __byte_perm(low, top, 0x7362);
+}
+
 // The scale of a block whose largest magnitude is `amax` (finite, >= 0).
 template <int FMT>
 __device__ __forceinline__ float scale_for(float amax) {
