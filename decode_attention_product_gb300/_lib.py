@@ -64,7 +64,7 @@ SIGNATURES = {
     "aq_q8_decode_attention": ([P, i32, i32, i32, i32, P, P, P, i64, P, i32, P, i32, f32, i32, P, P, sz, P, P], i32),
     "aq_pages_workspace": ([i32, i64, P], i32),
     "aq_pages_extend": ([i32, P, P, P, i32, i32, P, P, i64, P, i32, P, sz, P, P], i32),
-    "aq_pages_fork": ([i32, P, P, P, i32, i32, P, P, i64, P, sz, P, P], i32),
+    "aq_pages_fork": ([i32, P, P, P, i32, i32, P, P, i64, P, P], i32),
     "aq_pages_free": ([i32, P, P, P, i32, i32, P, P, i64, P, P], i32),
     "aq_pages_compact": ([P, i32, i32, P, P, i64, P, i32, P, sz, P, P], i32),
 }

@@ -337,15 +337,19 @@ def decode_attention_fp16(q: torch.Tensor, kv_pages: torch.Tensor, block_table: 
 # --------------------------------------------------------------------------
 # rotary positions
 # --------------------------------------------------------------------------
+_functions = {}
+
+
 def _launch(dev: int, name: str, *args) -> None:
     """Call the library's `name` with args and the stream, `dev` current."""
-    fn = getattr(_lib.load(), name)
-    stream = torch._C._cuda_getCurrentRawStream(dev)
+    fn = _functions.get(name)
+    if fn is None:
+        fn = _functions[name] = getattr(_lib.load(), name)
     if torch._C._cuda_getDevice() == dev:
-        st = fn(*args, stream)
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, stream)
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     if st != _lib.AQ_OK:
         _lib.check(st, name)
 
@@ -629,16 +633,14 @@ def pages_extend(rows: torch.Tensor, new_lens: torch.Tensor, block_table: torch.
 
 
 def pages_fork(src_rows: torch.Tensor, dst_rows: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
-               refcount: torch.Tensor, workspace: torch.Tensor | None = None,
-               status: torch.Tensor | None = None) -> None:
+               refcount: torch.Tensor, status: torch.Tensor | None = None) -> None:
     """Empty rows dst_rows (int32 [n]) become copies of src_rows, sharing their pages."""
     _need_rows(src_rows, dst_rows, "dst_rows")
     R, MP, NP = _need_table(block_table, seq_lens, refcount)
-    ws = _page_workspace(workspace, R, NP, src_rows.device)
     dev = _same_device(src_rows, dst_rows=dst_rows, block_table=block_table, seq_lens=seq_lens, refcount=refcount,
-                       workspace=ws, status=status)
+                       status=status)
     _launch(dev, "aq_pages_fork", src_rows.shape[0], src_rows.data_ptr(), dst_rows.data_ptr(), block_table.data_ptr(),
-            R, MP, seq_lens.data_ptr(), refcount.data_ptr(), NP, ws.data_ptr(), _bytes(ws), _addr(status))
+            R, MP, seq_lens.data_ptr(), refcount.data_ptr(), NP, _addr(status))
 
 
 def pages_free(rows: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor, refcount: torch.Tensor,
@@ -689,7 +691,7 @@ class PageTable:
         pages_extend(rows, new_lens, *self._state(), self._arr, self.workspace, self.status)
 
     def fork(self, src_rows, dst_rows):
-        pages_fork(src_rows, dst_rows, *self._state(), self.workspace, self.status)
+        pages_fork(src_rows, dst_rows, *self._state(), self.status)
 
     def free(self, rows, keep_lens=None):
         pages_free(rows, *self._state(), keep_lens, self.status)

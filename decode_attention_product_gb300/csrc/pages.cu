@@ -8,11 +8,12 @@
 // there is no free list whose order could, and refcounts change by integer
 // atomics only.
 //
-// "The k-th free page" is a prefix count over refcount.  One launch counts
-// tiles of 4096 pages (and, in its first CTA, prefix-sums what each row needs);
-// the next gives every tile its rank base from the tile counts and lists the
-// free pages by rank; the last takes each row's pages from that list, copies page
-// data and publishes lengths.  Each launch overlaps the end of the one before.
+// "The k-th free page" is a prefix count over refcount, in tiles of 4096 pages, one
+// CTA each.  For pools of up to kDirectTiles tiles every CTA sums the tiles before
+// its own itself (from L2); larger ones count the tiles in a launch before.  The
+// free pages are listed by rank, a first CTA prefix-sums what each row needs, and
+// the next launch takes each row's pages from that list, copies page data and
+// publishes lengths.  Each launch overlaps the end of the one before.
 #include "common.cuh"
 #include "internal.h"
 
@@ -23,6 +24,10 @@ namespace {
 constexpr int kThreads = 1024;
 constexpr int kTile = 4 * kThreads;
 constexpr int kMaxPools = 256;
+// Pools of up to 6 tiles are counted without a launch of its own.  An extend without /
+// with it, us: 4.1 / 5.6 at 1 tile, 5.6 / 6.2 at 6, 7.5 / 6.3 at 16; a compaction: 5.2 /
+// 6.8, 6.9 / 6.8, 9.1 / 7.0.
+constexpr int kDirectTiles = 6;
 constexpr int kCopyThreads = 256;
 
 struct PageParams {
@@ -145,11 +150,46 @@ __device__ __forceinline__ void begin() {
     grid_launch_dependents();
 }
 
-// First launch.  CTA 0 (extend): needs and their prefix.  The others: one tile.
-template <bool EXTEND>
+// The page counts of the tiles: free pages (FREE) or live ones.
+template <bool FREE>
+__device__ __forceinline__ int count4(const int4 &r) {
+    return FREE ? (r.x == 0) + (r.y == 0) + (r.z == 0) + (r.w == 0) : (r.x > 0) + (r.y > 0) + (r.z > 0) + (r.w > 0);
+}
+
+template <bool FREE>
 __global__ void __launch_bounds__(kThreads) pages_count_kernel(const __grid_constant__ PageParams p) {
     begin();
-    if (EXTEND && blockIdx.x == 0) {
+    int sum;
+    block_scan(count4<FREE>(tile_counts(p, blockIdx.x)), &sum);
+    if (threadIdx.x == 0) p.tiles[blockIdx.x] = sum;
+}
+
+// The pages counted in tiles before `t`, and in all of them (one scan of both).
+template <bool FREE>
+__device__ __forceinline__ int tiles_before(const PageParams &p, int t, int *total) {
+    unsigned long long both = 0, sum;
+    if (p.ntiles <= kDirectTiles) {
+#pragma unroll 4
+        for (int i = 0; i < p.ntiles; ++i) {
+            const unsigned long long x = static_cast<unsigned>(count4<FREE>(tile_counts(p, i)));
+            both += (x << 32) + (i < t ? x : 0u);
+        }
+    } else {
+        for (int i = threadIdx.x; i < p.ntiles; i += kThreads) {
+            const unsigned long long x = static_cast<unsigned>(p.tiles[i]);
+            both += (x << 32) + (i < t ? x : 0u);
+        }
+    }
+    block_scan(both, &sum);
+    *total = static_cast<int>(sum >> 32);
+    return static_cast<int>(sum & 0xffffffffu);
+}
+
+// An extend's free pages by rank (CTAs 1 on, a tile each) and the rows' needs with
+// their prefix (CTA 0).
+__global__ void __launch_bounds__(kThreads) pages_assign_kernel(const __grid_constant__ PageParams p) {
+    begin();
+    if (blockIdx.x == 0) {
         claim_rows(p, p.rows);
         long long base = 0;
         for (int i0 = 0; i0 < p.n; i0 += kThreads) {
@@ -163,43 +203,16 @@ __global__ void __launch_bounds__(kThreads) pages_count_kernel(const __grid_cons
         if (threadIdx.x == 0) p.off[p.n] = base;
         return;
     }
-    const int t = blockIdx.x - (EXTEND ? 1 : 0);
+    const int t = blockIdx.x - 1;
     const int4 r = tile_counts(p, t);
-    const int n = EXTEND ? (r.x == 0) + (r.y == 0) + (r.z == 0) + (r.w == 0) : (r.x > 0) + (r.y > 0) + (r.z > 0) + (r.w > 0);
-    int sum;
-    block_scan(n, &sum);
-    if (threadIdx.x == 0) p.tiles[t] = sum;
-}
-
-// Sum of the tile counts before tile `t`, and of all of them (one scan of both).
-__device__ __forceinline__ int tiles_before(const PageParams &p, int t, int *total) {
-    unsigned long long both = 0, sum;
-    for (int i = threadIdx.x; i < p.ntiles; i += kThreads) {
-        const unsigned long long x = static_cast<unsigned>(p.tiles[i]);
-        both += (x << 32) + (i < t ? x : 0u);
-    }
-    block_scan(both, &sum);
-    *total = static_cast<int>(sum >> 32);
-    return static_cast<int>(sum & 0xffffffffu);
-}
-
-// Second launch of an extend: the lowest free pages, by rank, as many as are needed.
-__global__ void __launch_bounds__(kThreads) pages_assign_kernel(const __grid_constant__ PageParams p) {
-    begin();
-    const int4 r = tile_counts(p, blockIdx.x);
-    const long long need = p.off[p.n];
-    int total;
-    const int base = tiles_before(p, blockIdx.x, &total);
-    if (blockIdx.x == 0 && threadIdx.x == 0) p.total[0] = total;
+    int total, sum;
+    const int base = tiles_before<true>(p, t, &total);
+    if (t == 0 && threadIdx.x == 0) p.total[0] = total;
+    int rank = base + block_scan(count4<true>(r), &sum);
     const int f[4] = {r.x == 0, r.y == 0, r.z == 0, r.w == 0};
-    int sum;
-    int rank = base + block_scan(f[0] + f[1] + f[2] + f[3], &sum);
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-        if (f[k]) {
-            if (rank < need) p.movers[rank] = blockIdx.x * kTile + 4 * threadIdx.x + k;
-            ++rank;
-        }
+        if (f[k]) p.movers[rank++] = t * kTile + 4 * threadIdx.x + k;
 }
 
 // Chunk c of page `from` to page `to`, by one warp: up to 8 loads of 16 bytes per
@@ -239,7 +252,7 @@ __global__ void __launch_bounds__(kCopyThreads) pages_grow_kernel(const __grid_c
     const int i = blockIdx.x, copy = p.info[i];
     if (copy < 0) return;
     const long long at = p.off[i], end = p.off[i + 1];
-    if (end > p.total[0] && end > at) {                // (a row that needs no page is served in any case)
+    if (end > (p.ntiles ? p.total[0] : 0) && end > at) {                // (a row that needs no page is served in any case)
         if (blockIdx.y == 0 && threadIdx.x == 0) flag_status(p.status, AQ_DEV_NO_PAGE);
         return;
     }
@@ -264,34 +277,37 @@ __global__ void __launch_bounds__(kCopyThreads) pages_grow_kernel(const __grid_c
         copy_chunk(pools, from, to, c, threadIdx.x & 31);
 }
 
-// Fork: which entries hold (the destination is an empty row, named once).
-__global__ void __launch_bounds__(kThreads) pages_fork_check_kernel(const __grid_constant__ PageParams p) {
+// Fork, a CTA per entry.  An entry whose destination is named before, or whose source
+// is a destination, is refused: no row is then both read and written.
+__global__ void __launch_bounds__(kThreads) pages_fork_kernel(const __grid_constant__ PageParams p) {
     begin();
-    claim_rows(p, p.args);
-    for (int i = threadIdx.x; i < p.n; i += kThreads) {
-        const int src = p.rows[i], dst = p.args[i];
-        int L = -1;
-        if (!row_ok(p, src) || !row_ok(p, dst) || __ldcg(&p.claim[dst]) != i || p.seq_lens[dst] != 0)
-            flag_status(p.status, AQ_DEV_BAD_ROW);
-        else if (!len_ok(p, p.seq_lens[src])) flag_status(p.status, AQ_DEV_BAD_LENGTH);
-        else L = p.seq_lens[src];
-        p.info[i] = L;
+    const int i = blockIdx.x, src = p.rows[i], dst = p.args[i];
+    bool clash = false;
+    for (int j = threadIdx.x; j < p.n; j += kThreads) {
+        const int d = p.args[j];
+        clash |= d == src || (j < i && d == dst);
     }
-}
-
-__global__ void __launch_bounds__(kCopyThreads) pages_fork_kernel(const __grid_constant__ PageParams p) {
-    begin();
-    const int i = blockIdx.x, L = p.info[i];
+    __shared__ int len;
+    if (threadIdx.x == 0) {
+        len = -1;
+        if (!row_ok(p, src) || !row_ok(p, dst) || p.seq_lens[dst] != 0) flag_status(p.status, AQ_DEV_BAD_ROW);
+        else if (!len_ok(p, p.seq_lens[src])) flag_status(p.status, AQ_DEV_BAD_LENGTH);
+        else len = p.seq_lens[src];
+    }
+    if (__syncthreads_or(clash)) {
+        if (threadIdx.x == 0) flag_status(p.status, AQ_DEV_BAD_ROW);
+        return;
+    }
+    const int L = len, n = (L + kPage - 1) / kPage;
     if (L < 0) return;
-    const int32_t *src = p.block_table + static_cast<size_t>(p.rows[i]) * p.max_pages;
-    int32_t *dst = p.block_table + static_cast<size_t>(p.args[i]) * p.max_pages;
-    if (blockIdx.y == 0 && threadIdx.x == 0) p.seq_lens[p.args[i]] = L;
-    const int n = (L + kPage - 1) / kPage;
-    for (int j = blockIdx.y * kCopyThreads + threadIdx.x; j < n; j += gridDim.y * kCopyThreads) {
-        const int pg = src[j];
-        dst[j] = pg;
+    const int32_t *from = p.block_table + static_cast<size_t>(src) * p.max_pages;
+    int32_t *to = p.block_table + static_cast<size_t>(dst) * p.max_pages;
+    for (int j = threadIdx.x; j < n; j += kThreads) {
+        const int pg = from[j];
+        to[j] = pg;
         if (pg < 0 || pg >= p.num_pages || atomicAdd(&p.refcount[pg], 1) <= 0) flag_status(p.status, AQ_DEV_BAD_PAGE);
     }
+    if (threadIdx.x == 0) p.seq_lens[dst] = L;
 }
 
 // Free: a row keeps its first `keep` tokens.  The atomic minimum makes a row
@@ -328,7 +344,7 @@ __global__ void __launch_bounds__(kThreads) pages_map_kernel(const __grid_consta
     begin();
     const int4 r = tile_counts(p, blockIdx.x);
     int live;
-    const int base = tiles_before(p, blockIdx.x, &live);
+    const int base = tiles_before<false>(p, blockIdx.x, &live);
     // live pages below N: whole tiles, and the part of the tile that holds N
     const int cut = live / kTile;
     int under = 0;
@@ -336,7 +352,11 @@ __global__ void __launch_bounds__(kThreads) pages_map_kernel(const __grid_consta
         const int4 s = tile_counts(p, cut);
         const int i = cut * kTile + 4 * threadIdx.x;
         int n = (s.x > 0 && i < live) + (s.y > 0 && i + 1 < live) + (s.z > 0 && i + 2 < live) + (s.w > 0 && i + 3 < live);
-        for (int t = threadIdx.x; t < cut; t += kThreads) n += p.tiles[t];
+        if (p.ntiles <= kDirectTiles) {
+            for (int t = 0; t < cut; ++t) n += count4<false>(tile_counts(p, t));
+        } else {
+            for (int t = threadIdx.x; t < cut; t += kThreads) n += p.tiles[t];
+        }
         block_scan(n, &under);
     } else {
         under = live;                                  // every page is live
@@ -514,9 +534,9 @@ aq_status aq_pages_extend(int32_t n, const int32_t *rows, const int32_t *new_len
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     // a page's chunks over at most 64 CTAs of 8 warps
     const int parts = (pl.first[num_pools] + 7) / 8;
-    cudaError_t e = launch_dependent(pages_count_kernel<true>, dim3(p.ntiles + 1), dim3(kThreads), 0, s, 1, p);
-    if (e == cudaSuccess)
-        e = launch_dependent(pages_assign_kernel, dim3(p.ntiles > 0 ? p.ntiles : 1), dim3(kThreads), 0, s, 1, p);
+    cudaError_t e = cudaSuccess;
+    if (p.ntiles > kDirectTiles) e = launch_dependent(pages_count_kernel<true>, dim3(p.ntiles), dim3(kThreads), 0, s, 1, p);
+    if (e == cudaSuccess) e = launch_dependent(pages_assign_kernel, dim3(p.ntiles + 1), dim3(kThreads), 0, s, 1, p);
     if (e == cudaSuccess)
         e = launch_dependent(pages_grow_kernel, dim3(n, parts < 1 ? 1 : parts > 64 ? 64 : parts), dim3(kCopyThreads), 0, s,
                              1, p, pl);
@@ -525,25 +545,15 @@ aq_status aq_pages_extend(int32_t n, const int32_t *rows, const int32_t *new_len
 
 aq_status aq_pages_fork(int32_t n, const int32_t *src_rows, const int32_t *dst_rows, int32_t *block_table,
                         int32_t num_rows, int32_t max_pages, int32_t *seq_lens, int32_t *refcount,
-                        int64_t num_pages, void *workspace, size_t workspace_bytes, int32_t *device_status,
-                        aq_stream_t stream) {
+                        int64_t num_pages, int32_t *device_status, aq_stream_t stream) {
     const aq_status st = check_pages(n, num_rows, max_pages, num_pages);
     if (st != AQ_OK) return st;
     if (n == 0) return AQ_OK;
     if (n > num_rows || !src_rows || !dst_rows || !block_table || !seq_lens || (num_pages > 0 && !refcount) || off16(refcount))
         return AQ_ERR_INVALID_ARGUMENT;
-    if (!workspace || workspace_bytes < workspace_ints(num_rows, num_pages) * sizeof(int32_t))
-        return AQ_ERR_WORKSPACE_TOO_SMALL;
-    if (off16(workspace)) return AQ_ERR_INVALID_ARGUMENT;
     const PageParams p = page_params(n, src_rows, dst_rows, block_table, num_rows, max_pages, seq_lens, refcount,
-                                     num_pages, workspace, device_status);
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    cudaError_t e = launch_dependent(pages_fork_check_kernel, dim3(1), dim3(kThreads), 0, s, 1, p);
-    const int parts = (max_pages + 4 * kCopyThreads - 1) / (4 * kCopyThreads);
-    if (e == cudaSuccess)
-        e = launch_dependent(pages_fork_kernel, dim3(n, parts < 1 ? 1 : parts > 64 ? 64 : parts), dim3(kCopyThreads), 0, s,
-                             1, p);
-    return done(e);
+                                     num_pages, nullptr, device_status);
+    return done(launch_dependent(pages_fork_kernel, dim3(n), dim3(kThreads), 0, reinterpret_cast<cudaStream_t>(stream), 1, p));
 }
 
 aq_status aq_pages_free(int32_t n, const int32_t *rows, const int32_t *keep_lens, int32_t *block_table,
@@ -575,7 +585,8 @@ aq_status aq_pages_compact(int32_t *block_table, int32_t num_rows, int32_t max_p
     const PagePools pl = page_pools(pools, num_pools);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const int table = num_rows < 152 ? num_rows : 152;
-    cudaError_t e = launch_dependent(pages_count_kernel<false>, dim3(p.ntiles), dim3(kThreads), 0, s, 1, p);
+    cudaError_t e = cudaSuccess;
+    if (p.ntiles > kDirectTiles) e = launch_dependent(pages_count_kernel<false>, dim3(p.ntiles), dim3(kThreads), 0, s, 1, p);
     if (e == cudaSuccess) e = launch_dependent(pages_map_kernel, dim3(p.ntiles), dim3(kThreads), 0, s, 1, p);
     if (e == cudaSuccess)
         e = launch_dependent(pages_move_kernel, dim3(table + 152 * 5), dim3(kCopyThreads), 0, s, 1, p, pl, table);

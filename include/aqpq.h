@@ -606,7 +606,8 @@ aq_status aq_q8_decode_attention(const aq_pq_config *cfg, int32_t format, int32_
  *   pools  host array of up to 256 caches whose pages move with the table's (all
  *          layers' pools, and page_scales beside code_pages): data [NP] pages of
  *          page_bytes each (a multiple of 4; base 16-byte aligned)
- *   workspace  >= aq_pages_workspace() bytes, no initialisation needed
+ *   workspace  >= aq_pages_workspace() bytes (extend, compact), no
+ *          initialisation needed
  *
  * aq_pages_extend  row rows[i] grows to new_lens[i] >= its length: missing pages
  *                  are allocated, and a partly filled last page that other rows
@@ -618,8 +619,9 @@ aq_status aq_q8_decode_attention(const aq_pq_config *cfg, int32_t format, int32_
  *                  before it, exceed the free ones sets AQ_DEV_NO_PAGE (one
  *                  that needs no page is served).
  * aq_pages_fork    the empty row dst_rows[i] becomes a copy of src_rows[i],
- *                  sharing all its pages.  A destination that is not empty, or
- *                  named before, sets AQ_DEV_BAD_ROW.
+ *                  sharing all its pages.  A destination that is not empty or
+ *                  named before, or a source that is a destination of the call,
+ *                  sets AQ_DEV_BAD_ROW.
  * aq_pages_free    row rows[i] keeps its first keep_lens[i] tokens (none with
  *                  keep_lens NULL; a longer length keeps all): pages behind them
  *                  lose a reference, their entries become -1.  A row may be
@@ -645,8 +647,7 @@ aq_status aq_pages_extend(int32_t n, const int32_t *rows, const int32_t *new_len
 aq_status aq_pages_fork(int32_t n, const int32_t *src_rows, const int32_t *dst_rows,
                         int32_t *block_table, int32_t num_rows, int32_t max_pages,
                         int32_t *seq_lens, int32_t *refcount, int64_t num_pages,
-                        void *workspace, size_t workspace_bytes, int32_t *device_status,
-                        aq_stream_t stream);
+                        int32_t *device_status, aq_stream_t stream);
 aq_status aq_pages_free(int32_t n, const int32_t *rows, const int32_t *keep_lens,
                         int32_t *block_table, int32_t num_rows, int32_t max_pages,
                         int32_t *seq_lens, int32_t *refcount, int64_t num_pages,

@@ -81,7 +81,7 @@ class Model:
         for s, d in zip(src, dst):
             first = d not in seen
             seen.add(d)
-            if not self.ok(s) or not self.ok(d) or not first or lens0[d] != 0:
+            if not self.ok(s) or not self.ok(d) or not first or lens0[d] != 0 or s in dst:
                 self.status |= BAD_ROW
                 continue
             n = pages_of(int(lens0[s]))
@@ -138,12 +138,13 @@ class Both:
         self.same()
 
 
-@pytest.mark.parametrize("seed,R,mp,NP", [(0, 12, 9, 60), (1, 40, 5, 150), (2, 3, 40, 64), (3, 200, 12, 5000), (4, 8, 3, 4096), (5, 6, 4, 4097)])
+@pytest.mark.parametrize("seed,R,mp,NP", [(0, 12, 9, 60), (1, 40, 5, 150), (2, 3, 40, 64), (3, 200, 12, 5000), (4, 8, 3, 4096),
+                                          (5, 6, 4, 4097), (6, 1500, 3, 6 * 4096), (7, 30, 6, 6 * 4096 + 1)])
 def test_random_runs_match_the_model(A, seed, R, mp, NP):
     """Random forks, growth, truncation, endings and compactions; pools run out
     now and then; rows repeat, lie outside, or break the rules."""
     g = np.random.default_rng(seed)
-    b = Both(A, R, mp, NP, seed=seed)
+    b = Both(A, R, mp, NP, (64, 4, 20) if NP > 20000 else (64, 4, 20, 4112), seed=seed)
     for _ in range(30):
         lens, n = b.m.lens, int(g.integers(1, R + 1))
         op = g.choice(["extend", "extend", "fork", "free", "truncate", "compact"])

@@ -147,8 +147,8 @@ def test_pages_refusals(lib):
     def ext(n=2, rows=FAKE, lens=FAKE, bt=FAKE, R=4, mp=8, sl=FAKE, rc=FAKE, NP=100, pools=None, k=0, ws=FAKE, wsb=1 << 20):
         return lib.aq_pages_extend(n, rows, lens, bt, R, mp, sl, rc, NP, pools, k, ws, wsb, None, None)
 
-    def fork(n=2, src=FAKE, dst=FAKE, bt=FAKE, R=4, mp=8, sl=FAKE, rc=FAKE, NP=100, ws=FAKE, wsb=1 << 20):
-        return lib.aq_pages_fork(n, src, dst, bt, R, mp, sl, rc, NP, ws, wsb, None, None)
+    def fork(n=2, src=FAKE, dst=FAKE, bt=FAKE, R=4, mp=8, sl=FAKE, rc=FAKE, NP=100):
+        return lib.aq_pages_fork(n, src, dst, bt, R, mp, sl, rc, NP, None, None)
 
     def free(n=2, rows=FAKE, keep=None, bt=FAKE, R=4, mp=8, sl=FAKE, rc=FAKE, NP=100):
         return lib.aq_pages_free(n, rows, keep, bt, R, mp, sl, rc, NP, None, None)
@@ -158,11 +158,11 @@ def test_pages_refusals(lib):
 
     for f in (ext, fork):
         for bad in (dict(n=-1), dict(n=5), dict(R=-1), dict(mp=-1), dict(NP=-1), dict(bt=None), dict(sl=None),
-                    dict(rc=None), dict(rc=ODD), dict(ws=ODD)):
+                    dict(rc=None), dict(rc=ODD)):
             assert f(**bad) == INV, (f, bad)
         assert f(NP=1 << 31) == UNS and f(mp=1 << 28) == UNS
-        assert f(ws=None) == WS and f(wsb=16) == WS
         assert f(n=0) == 0
+    assert ext(ws=None) == WS and ext(wsb=16) == WS and ext(ws=ODD) == INV
     assert ext(rows=None) == INV and ext(lens=None) == INV and fork(src=None) == INV and fork(dst=None) == INV
     for bad in (dict(n=-1), dict(R=-1), dict(mp=-1), dict(rows=None), dict(bt=None), dict(sl=None), dict(rc=None), dict(rc=ODD)):
         assert free(**bad) == INV, bad
