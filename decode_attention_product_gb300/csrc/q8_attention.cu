@@ -27,6 +27,18 @@
 // The splits of a (request, kv head) are the CTAs of a cluster, up to 8: their
 // results merge through distributed shared memory, in one launch and without
 // workspace.  More splits (few, very long requests) go through partials.
+//
+// Measured (INT8 unless said; of the measured copy rate): ragged (256 requests, 421 k
+// tokens, 32 heads, 3.5 GB) 523 us, 0.97; long (131072 tokens, 32 heads) 166 us with
+// the combine, 0.95 (E4M3 196 us: its widening's integer operations); page1 (4 x 2048
+// tokens, 32 heads) 17 us, 0.58; qwen_gqa (8 x 1000 tokens, 64 query and 8 kv heads,
+// E4M3) 9 us, 0.28; 512 tokens of 2 heads 3.7 us.  The large ones are bound by HBM;
+// the small ones by the chain release - ids and length - first page - merge, 5 to 6 us
+// of it without a page's work, and by issue while their few pages per warp run.
+// Tried and slower: pages loaded straight to registers (one page in flight per warp
+// at 158 registers: long 295 us), 8 splits pushed to their owners (a release barrier
+// in the prologue, 3 us under load), sums of the warps in row order (8-way bank
+// conflicts, 2 us at a group of 8).
 #include <cudaTypedefs.h>
 
 #include <cmath>

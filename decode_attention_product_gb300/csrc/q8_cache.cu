@@ -6,6 +6,12 @@
 // between warps.  Lane l holds dims [4l, 4l + 4) of every row: 8-byte fp16
 // loads, 4-byte code stores, whole 128-byte lines per row.
 //
+// Measured, 32 kv heads: append of 7.7 k tokens in 5 prompts (INT8) 37 us for 188 MB,
+// bound by issue (70 % of the slots: about 54 instructions per 128-element row) and
+// the chain of dependent loads before it; read-back of the same 40 us, bound by that
+// chain (request, length, page, codes); both in one graph 73 us, 0.76 of the copy
+// rate.  One token for each of 256 requests: append 7 us.
+//
 // A ragged call knows its requests only on the device (cu_tokens).  Request b
 // owns the work units from v_b = cu_tokens[b] / 16 + 2 b on: appending n tokens
 // touches at most n / 16 + 2 pages, which v_{b+1} - v_b never undercuts, so the
