@@ -1,16 +1,15 @@
 // q8_cache.cu -- the 8-bit block-scaled cache: append of new tokens and the
 // read-back of cached ones.
 //
-// Work is cut by block: one warp per (request, page, kv head, K or V), so a
-// block's scale and its up to 16 rows belong to one warp and nothing is shared
-// between warps.  Lane l holds dims [4l, 4l + 4) of every row: 8-byte fp16
-// loads, 4-byte code stores, whole 128-byte lines per row.
+// Work is cut by block: a warp, or half of one, per (request, page, kv head, K or V), so
+// a block's scale and its up to 16 rows belong to it and nothing is shared between
+// warps.
 //
 // Measured, 32 kv heads: append of 7.7 k tokens in 5 prompts (INT8) 37 us for 188 MB,
 // bound by issue (70 % of the slots: about 54 instructions per 128-element row) and
-// the chain of dependent loads before it; read-back of the same 40 us, bound by that
-// chain (request, length, page, codes); both in one graph 73 us, 0.76 of the copy
-// rate.  One token for each of 256 requests: append 7 us.
+// the chain of dependent loads before it; read-back of the same 34 us, bound by that
+// chain (request, length, page, codes).  One token for each of 256 requests: append 5
+// us, read-back of its blocks 14 us for 53 MB.
 //
 // A ragged call knows its requests only on the device (cu_tokens).  Request b
 // owns the work units from v_b = cu_tokens[b] / 16 + 2 b on: appending n tokens
@@ -40,6 +39,25 @@ struct Q8CacheParams {
     int64_t num_pages;
     int32_t batch, num_tokens, num_kv_heads, max_pages;
 };
+
+__device__ __forceinline__ float4 halves(uint2 u) {
+    const float2 a = h2_to_f2(u.x), b = h2_to_f2(u.y);
+    return make_float4(a.x, a.y, b.x, b.y);
+}
+
+__device__ __forceinline__ void load_row(const __half *src, uint2 (&x)[1]) { x[0] = ld_global_na_v2(src); }
+
+__device__ __forceinline__ void load_row(const __half *src, uint2 (&x)[2]) {
+    const uint4 v = ld_global_na_v4(src);
+    x[0] = make_uint2(v.x, v.y);
+    x[1] = make_uint2(v.z, v.w);
+}
+
+__device__ __forceinline__ void store_codes(uint32_t *dst, const uint32_t (&c)[1]) { *dst = c[0]; }
+
+__device__ __forceinline__ void store_codes(uint32_t *dst, const uint32_t (&c)[2]) {
+    *reinterpret_cast<uint2 *>(dst) = make_uint2(c[0], c[1]);
+}
 
 struct Unit {
     int page;                      // the block table's entry, not checked (kNoPage: no place in the cache)
@@ -108,35 +126,43 @@ __device__ __forceinline__ bool page_ok(const Q8CacheParams &p, const Unit &w, i
     return ok;
 }
 
-// ROWS: the most rows that a block gets from the call (16, or 1 for a decode
-// step's single tokens, which then needs few registers and fills the SMs).
+// ROWS: the most rows that a block gets from the call.  16: a warp per head and K or V,
+// 4 dims per lane (16 rows of 8 dims would hold 122 registers and half the warps: 45 us
+// against 37 us for the 5 prompts above).  1, a decode step's single tokens: lanes 0-15 a
+// head's key row, lanes 16-31 its value row, 8 dims each (5.0 us against 6.1 us for 256).
 template <int FMT, int ROWS>
 __global__ void __launch_bounds__(kThreads, ROWS == 1 ? 6 : 4) q8_append_kernel(const __grid_constant__ Q8CacheParams p) {
     constexpr int D = kHeadDim, P = kPage;
+    constexpr int DL = ROWS == 1 ? 8 : 4, LANES = D / DL, W = DL / 4;      // dims per lane, lanes per row, words of codes
     grid_dependency_wait();
     grid_launch_dependents();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % LANES;
     const Unit w = find_unit(p, blockIdx.x, lane);
-    const int pairs = 2 * p.num_kv_heads, n = w.n;
+    const int n = w.n, pairs = 2 * p.num_kv_heads;
     if (n == 0 || w.page == kNoPage) return;
-    for (int hp = blockIdx.y * kWarps + warp; hp < pairs; hp += gridDim.y * kWarps) {
-        const __half *src = p.kv + (static_cast<size_t>(w.row) * pairs + hp) * D + 4 * lane;
-        uint2 x[ROWS];
+    const size_t row = static_cast<size_t>(pairs) * D;
+    for (int hp = (blockIdx.y * kWarps + warp) * W + lane / LANES; hp < pairs; hp += gridDim.y * kWarps * W) {
+        const __half *src = p.kv + static_cast<size_t>(w.row) * row + static_cast<size_t>(hp) * D + DL * sub;
+        uint2 x[ROWS][W];
         uint32_t top = 0;                              // largest |half| bits of each 16-bit lane
 #pragma unroll
         for (int s = 0; s < ROWS; ++s) {
-            x[s] = make_uint2(0u, 0u);
-            if (s < n) x[s] = ld_global_na_v2(src + static_cast<size_t>(s) * pairs * D);
+#pragma unroll
+            for (int j = 0; j < W; ++j) x[s][j] = make_uint2(0u, 0u);
+            if (s < n) load_row(src + s * row, x[s]);
         }
         if (!page_ok(p, w, lane)) return;              // (the rows were on their way meanwhile)
         const size_t block = static_cast<size_t>(w.page) * pairs + hp;
-        uint32_t *dst = reinterpret_cast<uint32_t *>(p.pages + block * (P * D)) + lane;
+        uint32_t *dst = reinterpret_cast<uint32_t *>(p.pages + block * (P * D)) + W * sub;
         const float old = w.s0 > 0 ? p.scales[block] : 0.f;
 #pragma unroll
         for (int s = 0; s < ROWS; ++s)
-            top = __vmaxu2(top, __vmaxu2(x[s].x & 0x7fff7fffu, x[s].y & 0x7fff7fffu));
+#pragma unroll
+            for (int j = 0; j < W; ++j)
+                top = __vmaxu2(top, __vmaxu2(x[s][j].x & 0x7fff7fffu, x[s][j].y & 0x7fff7fffu));
         top = max(top & 0xffffu, top >> 16);
-        top = __reduce_max_sync(0xffffffffu, top);
+#pragma unroll
+        for (int off = 1; off < LANES; off *= 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
         // a block that holds a non-finite value is NaN as a whole (codes 0)
         const float want = top >= 0x7c00u ? __int_as_float(0x7fc00000)
                                           : scale_for<FMT>(__half2float(__ushort_as_half(static_cast<unsigned short>(top))));
@@ -145,12 +171,16 @@ __global__ void __launch_bounds__(kThreads, ROWS == 1 ? 6 : 4) q8_append_kernel(
             // four rows under way together; rolled, so that its code does not crowd out the rest
 #pragma unroll 1
             for (int s = 0; s < w.s0; s += 4) {
-                uint32_t c[4];
+                uint32_t c[4][W];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) c[j] = s + j < w.s0 ? dst[(s + j) * (D / 4)] : 0u;
+                for (int k = 0; k < 4; ++k)
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (s + j < w.s0) dst[(s + j) * (D / 4)] = rescale4<FMT>(c[j], old, scale);
+                    for (int j = 0; j < W; ++j) c[k][j] = s + k < w.s0 ? dst[(s + k) * (D / 4) + j] : 0u;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int j = 0; j < W; ++j)
+                        if (s + k < w.s0) dst[(s + k) * (D / 4) + j] = rescale4<FMT>(c[k][j], old, scale);
             }
         }
         const Encoder enc = encoder_of<FMT>(scale);
@@ -159,53 +189,66 @@ __global__ void __launch_bounds__(kThreads, ROWS == 1 ? 6 : 4) q8_append_kernel(
 #pragma unroll
         for (int s = 0; s < ROWS; ++s) {
             if (s < n) {
-                const float2 a = h2_to_f2(x[s].x), b = h2_to_f2(x[s].y);
-                bool again;
-                dst[s * (D / 4)] = encode4<FMT>(make_float4(a.x, a.y, b.x, b.y), enc, again);
-                redo |= again ? 1u << s : 0u;
+                uint32_t c[W];
+#pragma unroll
+                for (int j = 0; j < W; ++j) {
+                    bool again;
+                    c[j] = encode4<FMT>(halves(x[s][j]), enc, again);
+                    redo |= again ? 1u << s : 0u;
+                }
+                store_codes(dst + s * (D / 4), c);
             }
         }
         while (redo) {                                 // few rows, if any: fetched again, decided exactly
             const int s = __ffs(redo) - 1;
             redo &= redo - 1;
-            const uint2 y = ld_global_na_v2(src + static_cast<size_t>(s) * pairs * D);
-            const float2 a = h2_to_f2(y.x), b = h2_to_f2(y.y);
-            dst[s * (D / 4)] = encode4_exact<FMT>(make_float4(a.x, a.y, b.x, b.y), scale);
+            uint2 y[W];
+            load_row(src + s * row, y);
+#pragma unroll
+            for (int j = 0; j < W; ++j) dst[s * (D / 4) + j] = encode4_exact<FMT>(halves(y[j]), scale);
         }
-        if (lane == 0 && (w.s0 == 0 || scale != old)) p.scales[block] = scale;
+        if (sub == 0 && (w.s0 == 0 || scale != old)) p.scales[block] = scale;
     }
 }
 
+// The read-back: lanes 0-15 a head's key rows, lanes 16-31 its value rows, 8 dims each, so
+// that a token's row is 512 contiguous bytes (against 256 and 4 dims per lane: 34 us
+// against 41 us for the same prompts, 14 us against 19 us for the step's blocks).
 template <int FMT>
-__global__ void __launch_bounds__(kThreads, 6) q8_load_kernel(const __grid_constant__ Q8CacheParams p) {
+__global__ void __launch_bounds__(kThreads, 4) q8_load_kernel(const __grid_constant__ Q8CacheParams p) {
     constexpr int D = kHeadDim, P = kPage;
     grid_dependency_wait();
     grid_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const Unit w = find_unit(p, blockIdx.x, lane);
-    const int pairs = 2 * p.num_kv_heads, n = w.n;
+    const int n = w.n;
     if (n == 0) return;
     const bool bad = !page_ok(p, w, lane);
-    for (int hp = blockIdx.y * kWarps + warp; hp < pairs; hp += gridDim.y * kWarps) {
-        __half *dst = p.kv + (static_cast<size_t>(w.row) * pairs + hp) * D + 4 * lane;
-        const size_t block = static_cast<size_t>(bad ? 0 : w.page) * pairs + hp;
+    const size_t row = static_cast<size_t>(p.num_kv_heads) * 2 * D;
+    for (int h = blockIdx.y * kWarps + warp; h < p.num_kv_heads; h += gridDim.y * kWarps) {
+        __half *dst = p.kv + static_cast<size_t>(w.row) * row + static_cast<size_t>(h) * 2 * D + 8 * lane;
+        const size_t block = (static_cast<size_t>(bad ? 0 : w.page) * p.num_kv_heads + h) * 2 + (lane >> 4);
         const float scale = bad ? __int_as_float(0x7fc00000) : p.scales[block];
-        const uint32_t *src = reinterpret_cast<const uint32_t *>(p.pages + block * (P * D)) + w.s0 * (D / 4) + lane;
-        uint32_t c[P];
+        const uint8_t *src = p.pages + block * (P * D) + w.s0 * D + 8 * (lane & 15);
+        uint2 c[P];
 #pragma unroll
-        for (int s = 0; s < P; ++s) c[s] = !bad && s < n ? src[s * (D / 4)] : 0u;
+        for (int s = 0; s < P; ++s) {
+            c[s] = make_uint2(0u, 0u);
+            if (!bad && s < n) c[s] = ld_global_na_v2(src + s * D);
+        }
 #pragma unroll
         for (int s = 0; s < P; ++s) {
             if (s < n) {
-                uint32_t lo, hi;
-                widen4<FMT>(c[s], lo, hi);
-                const float2 a = h2_to_f2(lo), b = h2_to_f2(hi);
-                const __half2 l = __floats2half2_rn(a.x * scale, a.y * scale);
-                const __half2 h = __floats2half2_rn(b.x * scale, b.y * scale);
-                uint2 r;
-                r.x = *reinterpret_cast<const uint32_t *>(&l);
-                r.y = *reinterpret_cast<const uint32_t *>(&h);
-                *reinterpret_cast<uint2 *>(dst + static_cast<size_t>(s) * pairs * D) = r;
+                uint32_t v[4], r[4];
+                widen4<FMT>(c[s].x, v[0], v[1]);
+                widen4<FMT>(c[s].y, v[2], v[3]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 a = h2_to_f2(v[j]);
+                    const __half2 h2 = __floats2half2_rn(a.x * scale, a.y * scale);
+                    r[j] = *reinterpret_cast<const uint32_t *>(&h2);
+                }
+                *reinterpret_cast<uint4 *>(dst + s * row) = make_uint4(r[0], r[1], r[2], r[3]);
             }
         }
     }
@@ -242,7 +285,8 @@ aq_status q8_cache_call(bool append, const aq_pq_config *cfg, int32_t format, in
                                      : static_cast<unsigned>(batch);
     // a unit's heads over several CTAs only as far as that fills the GPU (6 CTAs per SM,
     // twice): a CTA's first loads depend on one another, its heads' do not
-    unsigned split = static_cast<unsigned>((2 * num_kv_heads + kWarps - 1) / kWarps);
+    const int warps = append && cu_tokens ? 2 * num_kv_heads : num_kv_heads;
+    unsigned split = static_cast<unsigned>((warps + kWarps - 1) / kWarps);
     if (split > 2u * 6u * 152u / units + 1u) split = 2u * 6u * 152u / units + 1u;
     const dim3 grid(units, split);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
