@@ -554,6 +554,8 @@ def q8_decode_attention(q: torch.Tensor, code_pages: torch.Tensor, page_scales: 
     else:
         _need(out, torch.float32, "out", 3)
         _shape(out, q.shape, "out")
+    if max_seq_len > 0x7fffffff or num_splits > 0x7fffffff:
+        raise ValueError("max_seq_len and num_splits are 32-bit numbers")
     need = q8_decode_plan(B, Hq, Hkv, max_seq_len, num_splits)[1]
     if workspace is None and need:
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)

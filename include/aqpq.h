@@ -487,7 +487,8 @@ aq_status aq_decode_attention_noalloc(const aq_pq_config *cfg, int32_t batch,
  *                   pass through unturned.  With AQ_ROPE_LENGTHS positions holds
  *                   sequence lengths and token t stands at positions[t] - 1
  *                   (a decode step's current tokens)
- *   inv_freq   in   double [rot_dim / 2] (device), from aq_rope_frequencies
+ *   inv_freq   in   double [rot_dim / 2] (device, 16-byte aligned), from
+ *                   aq_rope_frequencies
  *   q, q_out   fp32 [T][Hq][D], both or neither
  *   kv, kv_out fp16 [T][Hkv][2][D], both or neither; keys turn
  *   An output may be its input (in place: padding, values and unturned dims are
@@ -577,7 +578,9 @@ aq_status aq_q8_load(const aq_pq_config *cfg, int32_t format, int32_t batch,
  * tokens' codes stand for, any number of query heads per kv head (Hq a multiple
  * of Hkv).  Lengths, errors, splits, workspace and out as there; scales are
  * finite and >= 0, or NaN, which makes the outputs that read the block NaN.
- * aq_q8_decode_plan gives the splits and the workspace a call uses (host only).
+ * aq_q8_decode_plan gives the splits and the workspace a call uses (host only):
+ * none up to 8 splits.  Calls that may overlap on the GPU (other streams, graphs
+ * replayed side by side) need workspaces of their own, as everywhere.
  * ------------------------------------------------------------------------- */
 aq_status aq_q8_decode_plan(const aq_pq_config *cfg, int32_t batch, int32_t num_q_heads,
                             int32_t num_kv_heads, int32_t max_seq_len,
@@ -597,7 +600,8 @@ aq_status aq_q8_decode_attention(const aq_pq_config *cfg, int32_t format, int32_
  * §2.2.2: a global block table over a pool of pages).  Row r of the block table
  * [R][max_pages] holds the pages of a request with seq_lens[r] tokens (0: an
  * empty row): entries 0 .. ceil(seq_lens[r] / P) - 1 count, the others do not.
- * refcount int32 [NP] is the number of rows that hold a page; 0 means free.  The
+ * refcount int32 [NP] (16-byte aligned) is the number of rows that hold a page; 0
+ * means free.  The
  * calls change block_table, seq_lens and refcount in place; the caller starts
  * from an empty table (all lengths and refcounts 0).  New pages are the lowest
  * free ids, in the order of the call's rows.  Rows are device int32 arrays; each

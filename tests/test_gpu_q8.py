@@ -551,3 +551,83 @@ def test_attention_wait_limit(A):
             close(got[~bad.any(-1)], want[~bad.any(-1)], tol[~bad.any(-1)])
             seen |= flag
         assert seen == 8, splits
+
+
+@pytest.mark.parametrize("splits", [1, 4, 12])
+def test_attention_non_finite_queries_stay_in_their_heads(A, splits):
+    """An infinite or NaN query makes its own head's output NaN, no other's."""
+    g = np.random.default_rng(18)
+    for fmt in ("int8", "e4m3"):
+        p = problem(g, 2, 2, 8, [300, 17], fmt)
+        want, tol = reference(p)
+        p["q"][0, 3, 5], p["q"][0, 12, 100], p["q"][1, 0, 0] = np.inf, np.nan, -np.inf
+        got, st = attend(A, p, splits)
+        bad = np.zeros((2, 16), bool)
+        bad[0, 3] = bad[0, 12] = bad[1, 0] = True
+        assert st == 0 and np.isnan(got[bad]).all()
+        close(got[~bad], want[~bad], tol[~bad])
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_step_in_a_graph(A, fmt):
+    """Q8DecodeStep captured once and replayed while the requests grow equals the
+    calls made one by one."""
+    g = np.random.default_rng(19)
+    B, H, G, mp = 3, 2, 4, 6
+    rope = A.Rope(128, 1e4)
+    bt = dev(g.permutation(B * mp).reshape(B, mp).astype(np.int32))
+    caches = [A.new_q8_cache(B * mp, H, e4m3=fmt == "e4m3") for _ in range(2)]
+    lens = dev(np.array([30, 1, 15], np.int32))
+    kv0 = dev(draw_kv(g, 46, H))
+    cu = dev(np.array([0, 30, 31, 46], np.int32))
+    for pages, scales in caches:
+        A.q8_append(kv0, pages, scales, bt, lens, cu)
+    q, kv = torch.zeros(B, H * G, D, device="cuda"), torch.zeros(B, H, 2, D, dtype=torch.float16, device="cuda")
+    steps = [A.Q8DecodeStep(pages, scales, bt, lens, mp * P, H * G, rope=rope, num_splits=s) for (pages, scales), s in zip(caches, (0, 0))]
+    keep = [c.clone() for c in caches[0]]
+    lens += 1
+    steps[0].run(q, kv)                                                     # (loads the kernels)
+    lens -= 1
+    for c, k in zip(caches[0], keep):
+        c.copy_(k)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        lens += 1
+        steps[0].run(q, kv)
+    for _ in range(20):
+        q.copy_(dev(g.standard_normal((B, H * G, D)).astype(np.float32)))
+        kv.copy_(dev(draw_kv(g, B, H)))
+        graph.replay()
+        want = steps[1].run(q, kv)
+        assert torch.equal(steps[0].out, want)
+        assert torch.equal(caches[0][0], caches[1][0]) and torch.equal(caches[0][1], caches[1][1])
+    for s in steps:
+        s.check_status()
+    assert lens.tolist() == [50, 21, 35]
+
+
+def test_rows_past_32_bits(A):
+    """Appends and read-backs whose element offsets pass 2^31."""
+    T, H = 70001, 128                                                       # 2.3e9 halves
+    g = np.random.default_rng(20)
+    kv = torch.zeros((T, H, 2, D), dtype=torch.float16, device="cuda")
+    tail = draw_kv(g, 33, H)
+    kv[-33:] = dev(tail)
+    NP = -(-T // P)
+    pages, scales = A.new_q8_cache(NP, H)
+    bt, lens = dev(np.arange(NP, dtype=np.int32)[None]), dev(np.array([T], np.int32))
+    cu = dev(np.array([0, T], np.int32))
+    st = A.new_status()
+    A.q8_append(kv, pages, scales, bt, lens, cu, st)
+    back = A.q8_load(pages, scales, bt, lens, cu, T, status=st)
+    assert int(st.item()) == 0
+    small, ssc = np.zeros((4, H, 2, P, D), np.int8), np.zeros((4, H, 2), np.float32)
+    first = (T - 33) // P * P
+    x = np.concatenate([np.zeros((T - 33 - first, H, 2, D), np.float16), tail])
+    model_append(small, ssc, [0, 1, 2, 3], 0, x, "int8")
+    n = -(-len(x) // P)
+    assert np.array_equal(pages[-n:, :, :].cpu().numpy()[:-1], small[:n - 1])
+    assert np.array_equal(pages[-1, :, :, :(T - 1) % P + 1].cpu().numpy(), small[n - 1, :, :, :(T - 1) % P + 1])
+    assert np.array_equal(scales[-n:].cpu().numpy(), ssc[:n])
+    err = (back[-33:].float() - dev(tail).float()).abs()
+    assert float((err - 0.51 * scales[-n:].max()).max()) <= 0 and int(back[:first].count_nonzero()) == 0

@@ -202,3 +202,18 @@ def test_decode_step_with_rope(A):
     torch.cuda.synchronize()
     s1.check_status()
     assert torch.equal(got, want) and torch.equal(p1, p2) and not torch.equal(p1, d["code_pages"])
+
+
+def test_rope_past_32_bits(A):
+    """Rows whose element offset passes 2^31."""
+    T, H = 70001, 256                                                       # 2.3e9 elements
+    q = torch.zeros(T, H, 128, device="cuda")
+    g = np.random.default_rng(7)
+    tail = g.standard_normal((3, H, 128), np.float32)
+    q[-3:] = torch.from_numpy(tail).cuda()
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")
+    w = 10000.0 ** (-np.arange(0, 128, 2) / 128)
+    A.rope(pos, torch.from_numpy(w).cuda(), q, q_out=q)
+    want, tol = reference(tail, np.arange(T - 3, T), w, False, 1.0, False)
+    assert np.all(np.abs(q[-3:].cpu().numpy() - want) <= tol)
+    assert int(q[:-3].count_nonzero()) == 0
