@@ -546,24 +546,46 @@ __global__ void __launch_bounds__(kHeadDim) q8_combine_kernel(const __grid_const
     p.out[bh * kHeadDim + d] = nan ? __int_as_float(0x7fc00000) : den > 0.f ? num / den : 0.f;
 }
 
-// Splits of a call (host arithmetic): enough CTAs to fill the GPU (4 per SM),
-// each with a page per warp at least; up to kMaxCluster of them are a cluster.
+// Splits of a call (host arithmetic): the count with the least estimated time.  The
+// estimate, in ns, was fitted to timings of 12 shapes (8 to 608 units, 2048 to 60000
+// tokens, 1 to 64 splits): a CTA takes 180 per page while SMs hold one CTA, 220 with two,
+// 350 with up to four (by then the memory's rate), and a fixed 2100 alone, 3000 + 150 S
+// in a cluster of S, 5500 + 80 S with partials and their combine.  608 CTAs are a
+// wave.  Against whole powers of two up to a wave: 96 units of 8192 tokens 37 us (6
+// splits) instead of 49 (4), 192 of 2048 tokens 21 (3) instead of 27 (2), 8 of 4096
+// tokens 8.4 (16) instead of 10.8 (64).
 struct Q8Plan {
     int32_t num_splits;
     size_t workspace;
 };
+
+constexpr int64_t kSlots = 4 * 152;
+
+int64_t q8_estimate(int64_t units, int64_t pages, int64_t S) {
+    const int64_t per_cta = (pages + kWarps * S - 1) / (kWarps * S) * kWarps;
+    const int64_t fixed = S == 1 ? 2100 : S <= kMaxCluster ? 3000 + 150 * S : 5500 + 80 * S;
+    auto wave = [&](int64_t ctas) { return per_cta * (ctas <= kSlots / 4 ? 180 : ctas <= kSlots / 2 ? 220 : 350) + fixed; };
+    const int64_t ctas = units * S, rest = ctas % kSlots;
+    return ctas / kSlots * wave(kSlots) + (rest ? wave(rest) : 0);
+}
 
 Q8Plan q8_plan(int64_t batch, int64_t Hq, int64_t Hkv, int32_t max_seq_len, int32_t req) {
     const int64_t G = Hq / Hkv, units = batch * Hkv * ((G + kGroup - 1) / kGroup);
     const int64_t pages = (static_cast<int64_t>(max_seq_len) + kPage - 1) / kPage;
     int64_t S = req;
     if (S <= 0) {
-        const int64_t slots = 4 * 152, most = pages / kWarps;
-        S = units > 0 ? slots / units : 1;
-        if (S > most) S = most;
-        // one cluster of a power of two CTAs (they fit the GPU's groups of SMs
-        // evenly) until partials give twice as many
-        if (S > 1 && S < 2 * kMaxCluster) S = S >= 8 ? 8 : S >= 4 ? 4 : 2;
+        S = 1;
+        const int64_t most = pages / kWarps;           // a page per warp at least
+        auto consider = [&](int64_t c) {
+            if (c > 1 && c <= most && c <= 4096 && q8_estimate(units, pages, c) < q8_estimate(units, pages, S)) S = c;
+        };
+        if (units > 0) {
+            for (int64_t c = 2; c <= kMaxCluster; ++c) consider(c);
+            for (int64_t c = 12; c <= 32; c += 4) consider(c);
+            consider(kSlots / 4 / units);
+            consider(kSlots / 2 / units);
+            consider(kSlots / units);
+        }
     }
     if (S > 4096) S = 4096;
     if (S > pages) S = pages;

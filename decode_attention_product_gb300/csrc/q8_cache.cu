@@ -284,7 +284,9 @@ aq_status q8_cache_call(bool append, const aq_pq_config *cfg, int32_t format, in
     const unsigned units = cu_tokens ? static_cast<unsigned>(num_tokens / kPage) + 2u * batch + 1u
                                      : static_cast<unsigned>(batch);
     // a unit's heads over several CTAs only as far as that fills the GPU (6 CTAs per SM,
-    // twice): a CTA's first loads depend on one another, its heads' do not
+    // twice): a CTA's first loads depend on one another, its heads' do not.  (The 5
+    // prompts' append and the step's read-back: 37.5 and 14.2 us; filled once 38.7 and
+    // 15.1, four times 40.2 and 15.2)
     const int warps = append && cu_tokens ? 2 * num_kv_heads : num_kv_heads;
     unsigned split = static_cast<unsigned>((warps + kWarps - 1) / kWarps);
     if (split > 2u * 6u * 152u / units + 1u) split = 2u * 6u * 152u / units + 1u;
