@@ -29,10 +29,10 @@
 // workspace.  More splits (few, very long requests) go through partials.
 //
 // Measured (INT8 unless said; of the measured copy rate): ragged (256 requests, 421 k
-// tokens, 32 heads, 3.5 GB) 523 us, 0.97; long (131072 tokens, 32 heads) 166 us with
-// the combine, 0.95 (E4M3 196 us: its widening's integer operations); page1 (4 x 2048
-// tokens, 32 heads) 17 us, 0.58; qwen_gqa (8 x 1000 tokens, 64 query and 8 kv heads,
-// E4M3) 9 us, 0.28; 512 tokens of 2 heads 3.7 us.  The large ones are bound by HBM;
+// tokens, 32 heads, 3.5 GB) 511 us, 1.0; long (131072 tokens, 32 heads) 168 us with the
+// combine, 0.94 (E4M3 190 us: the ALU, its widening takes 15 integer operations where
+// INT8's takes 11); page1 (4 x 2048 tokens, 32 heads) 16.6 us, 0.60; qwen_gqa (8 x 1000
+// tokens, 64 query and 8 kv heads, E4M3) 8.7 us, 0.29; 512 tokens of 2 heads 3.7 us.  The large ones are bound by HBM;
 // the small ones by the chain release - ids and length - first page - merge, 5 to 6 us
 // of it without a page's work, and by issue while their few pages per warp run.
 // Tried and slower: pages loaded straight to registers (one page in flight per warp
@@ -120,8 +120,8 @@ __device__ __forceinline__ void cluster_arrive_release() {
 __device__ __forceinline__ uint32_t word(const uint4 &v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
 // The codes as fp16 operands: INT8 as they are, E4M3 times 2^-8 by integer operations
-// (long E4M3: 196 us against 203 us with the conversion instruction, whose rate is
-// lower than that of the six integer operations).
+// (the conversion instruction takes as long, long E4M3 189 against 190 us, but turns the
+// NaN codes that unused slots may hold into NaN, which would have to be masked).
 template <int FMT>
 constexpr float kUnwiden = FMT == kE4m3 ? 256.f : 1.f;
 
@@ -557,9 +557,9 @@ __global__ void __launch_bounds__(kHeadDim) q8_combine_kernel(const __grid_const
 // tokens, 1 to 64 splits): a CTA takes 180 per page while SMs hold one CTA, 220 with two,
 // 350 with up to four (by then the memory's rate), and a fixed 2100 alone, 3000 + 150 S
 // in a cluster of S, 5500 + 80 S with partials and their combine.  608 CTAs are a
-// wave.  Against whole powers of two up to a wave: 96 units of 8192 tokens 37 us (6
-// splits) instead of 49 (4), 192 of 2048 tokens 21 (3) instead of 27 (2), 8 of 4096
-// tokens 8.4 (16) instead of 10.8 (64).
+// wave.  Against whole powers of two up to a wave: 96 units of 8192 tokens 36 us (6
+// splits) instead of 47 (4), 192 of 2048 tokens 21 (3) instead of 27 (2), 8 of 4096
+// tokens 7.9 (16) instead of 10.8 (64).
 struct Q8Plan {
     int32_t num_splits;
     size_t workspace;
