@@ -189,9 +189,11 @@ __global__ void __launch_bounds__(kThreads, 4) q8_attention_kernel(const __grid_
         const int pg = i < p.max_pages ? bt[i] : -1;
         return pg >= 0 && pg < p.num_pages ? pg : -1;
     };
+    // (a coherent load: the kernel may be resident while the one before still writes scales)
     auto page_scales = [&](int pg) {
-        return pg >= 0 ? __ldg(reinterpret_cast<const float2 *>(p.scales) + static_cast<size_t>(pg) * p.num_kv_heads + kvh)
-                       : make_float2(0.f, 0.f);
+        if (pg < 0) return make_float2(0.f, 0.f);
+        const uint2 u = ld_global_na_v2(p.scales + (static_cast<size_t>(pg) * p.num_kv_heads + kvh) * 2);
+        return make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
     };
     int id = page_id(lane);
     const int L = p.seq_lens[b];
@@ -438,13 +440,11 @@ __global__ void __launch_bounds__(kThreads, 4) q8_attention_kernel(const __grid_
             f[w] = lw != lw ? lw : wm[w][g] > -INFINITY ? fast_exp2(wm[w][g] - ms) : 0.f;
             const float4 x = *reinterpret_cast<const float4 *>(
                 ring + static_cast<size_t>(w) * kStages * kPageBytes + (g * kSumPitch + 4 * lane) * 4);
-            if (f[w] != 0.f) {                         // (a warp without pages has nothing)
-                den += f[w] * lw;
-                num.x += f[w] * x.x;
-                num.y += f[w] * x.y;
-                num.z += f[w] * x.z;
-                num.w += f[w] * x.w;
-            }
+            den += f[w] * lw;                          // (a warp without pages adds 0 * 0; a NaN stays one)
+            num.x += f[w] * x.x;
+            num.y += f[w] * x.y;
+            num.z += f[w] * x.z;
+            num.w += f[w] * x.w;
         }
         if (merge) {
             *reinterpret_cast<float4 *>(co + g * D + 4 * lane) = num;
@@ -542,7 +542,7 @@ __global__ void __launch_bounds__(kHeadDim) q8_combine_kernel(const __grid_const
         __syncthreads();
 #pragma unroll 8
         for (int s = 0; s < n; ++s)
-            if (wgt[s] > 0.f) num += wgt[s] * po[static_cast<size_t>(s0 + s) * kHeadDim];
+            num += wgt[s] * po[static_cast<size_t>(s0 + s) * kHeadDim];    // (an empty split: 0 * 0)
     }
 #pragma unroll
     for (int off = 16; off; off /= 2) den += __shfl_xor_sync(0xffffffffu, den, off);

@@ -100,7 +100,7 @@ const char *aq_version(void);
 
 /* Limit, in nanoseconds, of the decode kernels' waits on their own
  * asynchronous copies (aq_decode_attention, aq_decode_step, the PQ part of
- * aq_decode_step_mixed); default AQ_DEFAULT_WAIT_LIMIT_NS (200 ms), at most
+ * aq_decode_step_mixed, aq_q8_decode_attention); default AQ_DEFAULT_WAIT_LIMIT_NS (200 ms), at most
  * 1 s.  A wait that runs out sets AQ_DEV_TIMEOUT, the outputs it affects
  * become NaN, and a fused step writes no new codes from that CTA.  Whatever
  * the limit, a kernel waits (up to 200 ms) for every copy into its shared

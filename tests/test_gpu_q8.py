@@ -631,3 +631,18 @@ def test_rows_past_32_bits(A):
     assert np.array_equal(scales[-n:].cpu().numpy(), ssc[:n])
     err = (back[-33:].float() - dev(tail).float()).abs()
     assert float((err - 0.51 * scales[-n:].max()).max()) <= 0 and int(back[:first].count_nonzero()) == 0
+
+
+@pytest.mark.parametrize("splits", [1, 4, 12])
+def test_nan_block_of_no_weight_is_not_lost(A, splits):
+    """A NaN value block whose tokens' weights vanish still makes its outputs NaN."""
+    g = np.random.default_rng(21)
+    p = problem(g, 1, 2, 2, [900], "int8")
+    p["pages"][:, 0, 0] = 0
+    pg = p["bt"][0, 5]
+    p["pages"][p["bt"][0, 40], 0, 0, 3] = 127                               # one key far ahead of all others
+    p["scales"][:, 0, 0] = 10.0
+    p["q"][0, :2] = 10.0
+    p["scales"][pg, 0, 1] = np.nan
+    got, st = attend(A, p, splits)
+    assert st == 0 and np.isnan(got[0, :2]).all() and np.isfinite(got[0, 2:]).all()
